@@ -334,6 +334,144 @@ VL_API vl_status vl_head_kl(const uint16_t* hidden, int64_t hs, const uint16_t* 
 VL_API vl_status vl_acc_add(float* a, const float* b, int64_t n, void* stream);
 
 /*
+ * ---------------------------------------------------------------- post-training
+ *
+ * Policy and preference training over the same rows of logits, the layer norm in front of
+ * the head, and the head's product in 8-bit floating point.  No counterpart on the pages;
+ * the formulas stand with each call.  The conventions above hold; in these calls:
+ *  - `weight` [ntok] fp32 takes the place of the loss window: a row of weight 0 (a prompt
+ *    or padding token) is not read at all (its logits may be anything, NaN included), has
+ *    loss, log-probability and KL 0 and a zero gradient row.
+ *  - `grad` [ntok][ldg] receives the gradient of the logits, in the logits' type; it may be
+ *    `logits` itself (then ldg == ld: in place), must not overlap it otherwise, and may be
+ *    NULL where no gradient is wanted.  Writes are 16 bytes wide when grad and logits rows
+ *    agree in their alignment modulo 16 bytes, else narrower (same results).
+ *  - a logit of -inf is an ordinary value (probability 0).
+ *  - scaling logits by a temperature belongs to the head's product (its alpha).
+ */
+
+/*
+ * Clipped policy loss with a KL term, forward and backward, over rows of logits.  Per row t
+ * with weight w != 0 (a = actions[t], A = adv[t]):
+ *     logp  = s[a] - lse                      r  = exp(logp - old_logp[t])
+ *     pg    = -min(r A, clip(r, 1 - clip_lo, 1 + clip_hi) A)
+ *     kl    = exp(q) - q - 1, q = ref_logp[t] - logp     (0 when ref_logp is NULL)
+ *     loss  = w (pg + kl_coef kl)
+ *     G     = d loss / d logp = w (-[r A not above its clipped value] r A + kl_coef (1 - exp(q)))
+ *     grad[t][j] = scale G ([j == a] - softmax(s)_j)
+ * The weights carry the mask and the averaging (over tokens, sequences or groups alike).
+ *   actions [ntok] u32; old_logp, adv, weight [ntok] fp32; ref_logp [ntok] fp32 (nullable);
+ *   0 <= clip_lo <= 1, clip_hi >= 0 (a positive infinity switches that side's clip off).
+ *   loss [ntok] fp32; logp, kl [ntok] fp32 (nullable); total: one fp32, the sum of loss
+ *   (nullable); err: one int32 (nullable).
+ * A row whose factor scale * G is 0 (a clipped one) has a gradient row of zeros.  An action
+ * >= V is counted in *err; its loss and logp are NaN, its gradient row is zero.
+ * Rows of up to VL_POLICY_ONEPASS_COLS columns are read from HBM once; longer ones twice.
+ */
+#define VL_POLICY_ONEPASS_COLS 245760
+VL_API vl_status vl_policy_loss(const float* logits, int64_t ld, int64_t ntok, int64_t V,
+                         const uint32_t* actions, const float* old_logp, const float* ref_logp,
+                         const float* adv, const float* weight, float clip_lo, float clip_hi, float kl_coef,
+                         float scale, float* grad, int64_t ldg, float* loss, float* logp, float* kl,
+                         float* total, int32_t* err, void* stream);
+VL_API vl_status vl_policy_loss_bf16(const uint16_t* logits, int64_t ld, int64_t ntok, int64_t V,
+                         const uint32_t* actions, const float* old_logp, const float* ref_logp,
+                         const float* adv, const float* weight, float clip_lo, float clip_hi, float kl_coef,
+                         float scale, uint16_t* grad, int64_t ldg, float* loss, float* logp, float* kl,
+                         float* total, int32_t* err, void* stream);
+
+/*
+ * Preference loss over pairs of sequences, forward and backward.  The rows of sequence s,
+ * s < 2 npairs, are [seq_start[s], seq_start[s + 1]); pair i prefers sequence i (chosen) to
+ * sequence npairs + i (rejected), as a concatenated batch lays them.  With logp_t the
+ * log-probability of labels[t]:
+ *     pi_s  = sum over its rows of weight_t logp_t      (weights 1, or 1 / length for a mean)
+ *     gap_i = (pi_i - ref_i) - (pi_{npairs+i} - ref_{npairs+i}),   h = beta gap
+ *     VL_PREF_SIGMOID  loss = -(1 - smooth) ln sigmoid(h) - smooth ln sigmoid(-h)
+ *     VL_PREF_IPO      loss = (gap - 1 / (2 beta))^2                  (smooth is not used)
+ *     VL_PREF_HINGE    loss = max(0, 1 - h)                           (smooth is not used)
+ *     grad[t][j] = scale (d loss_i / d pi_s) weight_t ([j == labels[t]] - softmax(s_t)_j)
+ * (scale = 1 / npairs gives the gradient of the mean.)  Sequence sums are taken in 64 bits in
+ * a fixed order.
+ *   labels [ntok] u32; weight [ntok] fp32; seq_start [2 npairs + 1] int64, ascending, in
+ *   [0, ntok] (values outside are clamped; rows of no sequence get a zero gradient);
+ *   ref_logp [2 npairs] fp32, the reference model's pi_s (nullable: zeros).
+ *   beta > 0, 0 <= smooth < 1.  npairs >= 1 unless ntok == 0.
+ *   loss, margin (= h) [npairs] fp32; seq_logp (pi_s) [2 npairs] fp32 (nullable); mean: one
+ *   fp32, the mean of loss (nullable); err: one int32 (nullable).
+ *   workspace: vl_preference_workspace_bytes(ntok, npairs) bytes of device memory, 16-byte
+ *   aligned, no initial contents needed; calls that share one must not overlap on the GPU.
+ * A pair with a label >= V (in a row of weight != 0) has loss, margin and pi_s NaN and zero
+ * gradient rows; each such label is counted in *err.
+ */
+typedef enum vl_pref_kind { VL_PREF_SIGMOID = 0, VL_PREF_IPO = 1, VL_PREF_HINGE = 2 } vl_pref_kind;
+VL_API int64_t vl_preference_workspace_bytes(int64_t ntok, int64_t npairs);
+VL_API vl_status vl_preference_loss(const float* logits, int64_t ld, int64_t ntok, int64_t V,
+                         const uint32_t* labels, const float* weight, const int64_t* seq_start, int64_t npairs,
+                         const float* ref_logp, float beta, float smooth, int kind, float scale,
+                         float* grad, int64_t ldg, float* loss, float* margin, float* seq_logp, float* mean,
+                         int32_t* err, void* workspace, int64_t workspace_bytes, void* stream);
+VL_API vl_status vl_preference_loss_bf16(const uint16_t* logits, int64_t ld, int64_t ntok, int64_t V,
+                         const uint32_t* labels, const float* weight, const int64_t* seq_start, int64_t npairs,
+                         const float* ref_logp, float beta, float smooth, int kind, float scale,
+                         uint16_t* grad, int64_t ldg, float* loss, float* margin, float* seq_logp, float* mean,
+                         int32_t* err, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Layer norm over rows of hs elements (the norm in front of the head):
+ *     mu = mean(x), rstd = 1 / sqrt(mean((x - mu)^2) + eps), xh = (x - mu) rstd
+ *     y  = xh gamma + beta
+ *   x [rows][ldx], y [rows][ldy] fp32, or bf16 in the _bf16 calls (sums in fp32, each output
+ *   rounded once); gamma, beta [hs] fp32 (nullable: 1 and 0); mu, rstd [rows] fp32 (nullable).
+ *   y may be x itself (ldy == ldx).  1 <= hs <= VL_NORM_MAX_HS; any alignment and strides.
+ * Backward, with t = dy gamma:
+ *     dx = rstd (t - mean(t) - xh mean(t xh)),  dgamma = sum over rows of dy xh,  dbeta = sum of dy
+ *   dy fp32 (in the _bf16 call: bf16, or fp32 when dy_f32 != 0, as the head's products hand
+ *   it back); mu, rstd as the forward pass wrote them; dx in x's type, may be x itself, or dy
+ *   when the types agree (then with the same stride); dgamma, dbeta [hs] fp32 (nullable), summed in a fixed
+ *   order: the same bits on every call.  With rows == 0 they are set to 0.
+ *   workspace: vl_layernorm_bwd_workspace_bytes(rows, hs) bytes, 16-byte aligned, needed when
+ *   dgamma or dbeta is given; calls that share one must not overlap on the GPU.
+ */
+#define VL_NORM_MAX_HS 16384
+VL_API vl_status vl_layernorm_fwd(const float* x, int64_t ldx, int64_t rows, int64_t hs, const float* gamma,
+                         const float* beta, float eps, float* y, int64_t ldy, float* mu, float* rstd, void* stream);
+VL_API vl_status vl_layernorm_fwd_bf16(const uint16_t* x, int64_t ldx, int64_t rows, int64_t hs, const float* gamma,
+                         const float* beta, float eps, uint16_t* y, int64_t ldy, float* mu, float* rstd, void* stream);
+VL_API int64_t vl_layernorm_bwd_workspace_bytes(int64_t rows, int64_t hs);
+VL_API vl_status vl_layernorm_bwd(const float* dy, int64_t lddy, const float* x, int64_t ldx, int64_t rows, int64_t hs,
+                         const float* gamma, const float* mu, const float* rstd, float* dx, int64_t lddx,
+                         float* dgamma, float* dbeta, void* workspace, int64_t workspace_bytes, void* stream);
+VL_API vl_status vl_layernorm_bwd_bf16(const void* dy, int dy_f32, int64_t lddy, const uint16_t* x, int64_t ldx,
+                         int64_t rows, int64_t hs, const float* gamma, const float* mu, const float* rstd,
+                         uint16_t* dx, int64_t lddx, float* dgamma, float* dbeta, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/*
+ * The head's product in 8-bit floating point (e4m3) with a scale for each block of 128 of the
+ * contraction: D[m][n] = alpha sum over k-blocks b of sa[b][m] sb[n / 128][b]
+ * sum over k in b of A[m][k] B[n][k].  Each block's sum comes from the tensor cores; the
+ * scaled sum over blocks is kept in fp32.
+ *   A [M][K], B [N][K] e4m3 bytes, row-major, 16-byte aligned, K a multiple of 16;
+ *   sa [ceil(K/128)][M], sb [ceil(N/128)][ceil(K/128)] fp32; D [M][ldd] fp32.
+ * With a frozen head: logits = hidden . W^T; and dx = g . Wt^T over the transposed plane Wt
+ * [hs][V], whose 128 x 128 blocks have the transposed scales.
+ *
+ * The quantisers: over each block, scale = max(amax, 2^-100) / 448 and q = x / scale rounded
+ * to the nearest e4m3 (ties to even), both divisions in fp32.  A NaN stays NaN, an infinity
+ * makes its block's values 0 or NaN with an infinite scale, so that the product is NaN.
+ * vl_quant_fp8_rows (fp32 x) / _bf16: blocks of 1 x 128, x [M][ldx] -> q [M][K], sa as above.
+ * vl_quant_fp8_blocks_bf16: blocks of 128 x 128, w [N][K] bf16 (contiguous) -> q [N][K], sb.
+ */
+VL_API vl_status vl_quant_fp8_rows(const float* x, int64_t ldx, int64_t M, int64_t K, uint8_t* q, float* sa,
+                         void* stream);
+VL_API vl_status vl_quant_fp8_rows_bf16(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, uint8_t* q, float* sa,
+                         void* stream);
+VL_API vl_status vl_quant_fp8_blocks_bf16(const uint16_t* w, int64_t N, int64_t K, uint8_t* q, float* sb, void* stream);
+VL_API vl_status vl_gemm_fp8_tn(const uint8_t* A, const float* sa, const uint8_t* B, const float* sb, float* D,
+                         int64_t M, int64_t N, int64_t K, int64_t ldd, float alpha, void* stream);
+
+/*
  * Test hook for the failure path (no counterpart on the pages).  Arms the next row-engine
  * launch (vl_ce_fwd, vl_ce_bwd_inplace, vl_ce_fused, vl_kl_topk_inplace) made from the
  * calling host thread: CTA 0 of that launch stops issuing its row tiles at body tile

@@ -92,4 +92,77 @@ int head_kl(const uint16_t* hidden, long long hs, const uint16_t* w, const uint1
             const uint32_t* labels, const uint32_t* tid, const float* tp, int k, float coef, float ce_coef,
             float dx_scale, long long ls, long long le, float* dx, float* kl_loss, float* ce_loss, float* ce_mean,
             int32_t* err, void* ws, long long ws_bytes, cudaStream_t st, char* msg, size_t msg_len);
+
+// Post-training losses over rows of logits (post.cu).
+struct PostParams {
+    const void* x;            // logits (fp32 or bf16, as dtype)
+    int dtype;
+    long long ld, ntok, V;
+    const uint32_t* label;    // actions / labels
+    const float* weight;
+    const float* old_logp;    // policy
+    const float* ref_logp;    // policy (nullable)
+    const float* adv;         // policy
+    float lo, hi, kl_coef;    // policy: the clip's ends 1 - clip_lo, 1 + clip_hi
+    float scale;              // of the gradient
+    void* g;                  // gradient (nullable)
+    long long ldg;
+    float* loss;              // policy [ntok]
+    float* logp;              // [ntok] (nullable for policy)
+    float* kl;                // policy (nullable)
+    float* stats;             // preference: (m, lnS) of each row
+    float* coef;              // preference: d(scaled loss)/d logp of each row
+    int* err;
+};
+
+struct PairParams {
+    const float* weight;
+    const float* logp;        // [ntok]
+    float* coef;              // [ntok]: in, 1 where the row's label is bad; out, the row's factor
+    const long long* start;   // [2 npairs + 1]
+    const float* ref;         // [2 npairs] (nullable)
+    long long ntok, npairs;
+    float beta, smooth, scale;
+    int kind;
+    float* loss;
+    float* margin;
+    float* seq;               // nullable
+};
+
+cudaError_t launch_policy(const PostParams& P, float* total, cudaStream_t st);
+cudaError_t launch_preference(const PostParams& P, const PairParams& Q, cudaStream_t st);
+
+// Layer norm (norm.cu); dtype is x's (and y's, dx's).
+struct NormParams {
+    const void* x;
+    int dtype;
+    long long ldx, rows;
+    int hs;
+    const float* gamma;       // nullable
+    const float* beta;        // nullable
+    float eps;
+    void* y;                  // forward: y; backward: dx
+    long long ldy;
+    float* mu_out;            // forward (nullable)
+    float* rstd_out;
+    const void* dy;           // backward
+    int dy_f32;
+    long long lddy;
+    const float* mu;
+    const float* rstd;
+    float* dgamma;            // nullable
+    float* dbeta;
+    float* part;              // workspace: partial sums of dgamma, dbeta
+};
+long long norm_bwd_ws_bytes(long long rows, long long hs);
+cudaError_t launch_norm_fwd(const NormParams& P, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormParams& P, cudaStream_t st);
+
+// 8-bit head product (fp8.cu).
+cudaError_t launch_quant_rows(const void* x, int dtype, long long ldx, long long M, long long K, uint8_t* q, float* sa,
+                              cudaStream_t st);
+cudaError_t launch_quant_blocks(const void* w, long long N, long long K, uint8_t* q, float* sb, cudaStream_t st);
+cudaError_t fp8_gemm_tn(const uint8_t* A, const float* sa, const uint8_t* B, const float* sb, float* D, long long M,
+                        long long N, long long K, long long ldd, float alpha, cudaStream_t st);
+unsigned int fp8_watchdog(bool clear);
 }  // namespace vl

@@ -1,5 +1,6 @@
 // C ABI of libvloss: argument checks on the host, launch choice, small kernels
 // (acc_add, windowed mean).  Declarations and contracts: include/vloss.h.
+#include "vl_api.h"
 #include "vl_device.cuh"
 #include "vl_internal.h"
 #include "vloss.h"
@@ -12,9 +13,8 @@
 #include <string>
 
 namespace vl {
-namespace {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
 vl_status fail(vl_status s, const char* fmt, ...) {
     char buf[512];
@@ -30,9 +30,22 @@ vl_status cuda_fail(cudaError_t e, const char* where) {
     return fail(VL_ELAUNCH, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-vl_status ok() { return VL_OK; }
+int num_sms() {
+    static std::atomic<int> cache[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64) {
+        const int c = cache[dev].load(std::memory_order_acquire);
+        if (c > 0) return c;
+    }
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64) cache[dev].store(sms, std::memory_order_release);
+    return sms;
+}
 
-cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
+namespace {
+
+vl_status ok() { return VL_OK; }
 
 // Longest row: the kernels index a row with 32-bit ints and step through it in
 // tiles of a few thousand columns, so a row stays 2^16 columns short of 2^31.
@@ -58,19 +71,6 @@ vl_status check_slice(int64_t col0, int64_t ncols, int64_t V, const char* fn) {
         return fail(VL_EINVAL, "%s: slice [%lld, %lld) not inside [0, %lld)", fn, (long long)col0,
                     (long long)(col0 + ncols), (long long)V);
     return ok();
-}
-
-int num_sms() {
-    static std::atomic<int> cache[64];
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (dev >= 0 && dev < 64) {
-        const int c = cache[dev].load(std::memory_order_acquire);
-        if (c > 0) return c;
-    }
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (dev >= 0 && dev < 64) cache[dev].store(sms, std::memory_order_release);
-    return sms;
 }
 
 // Grid of a launch.  Streaming modes: one CTA per SM (or per row when there are
@@ -221,6 +221,8 @@ __global__ void __launch_bounds__(1024) mean_kernel(const float* __restrict__ lo
     }
 }
 
+}  // namespace
+
 cudaError_t launch_mean(const float* loss, long long ls, long long le, float* mean, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, 1);
@@ -234,6 +236,8 @@ cudaError_t launch_mean(const float* loss, long long ls, long long le, float* me
     void* args[] = {(void*)&loss, (void*)&ls, (void*)&le, (void*)&mean};
     return cudaLaunchKernelExC(&cfg, (const void*)mean_kernel, args);
 }
+
+namespace {
 
 RowParams base_params(const void* logits, int dtype, int64_t ld, int64_t ntok, int64_t V) {
     RowParams P;
@@ -784,10 +788,13 @@ int vl_watchdog_flag(int device, int clear) {
         return -1;
     }
     const unsigned int a = rows_watchdog(clear != 0), b = topk_watchdog(clear != 0),
-                       c = topk_stream_watchdog(clear != 0), d = gemm_watchdog(clear != 0);
+                       c = topk_stream_watchdog(clear != 0), d = gemm_watchdog(clear != 0),
+                       e = fp8_watchdog(clear != 0);
     cudaSetDevice(prev);
-    if (a == 0xffffffffu || b == 0xffffffffu || c == 0xffffffffu || d == 0xffffffffu) return -1;
-    return (int)((a | b | c | d) & 0x7fffffffu);
+    if (a == 0xffffffffu || b == 0xffffffffu || c == 0xffffffffu || d == 0xffffffffu ||
+        e == 0xffffffffu)
+        return -1;
+    return (int)((a | b | c | d | e) & 0x7fffffffu);
 }
 
 }  // extern "C"

@@ -24,10 +24,14 @@ VL_OK, VL_EINVAL, VL_ELAUNCH, VL_EUNSUPPORTED = 0, 1, 2, 3
 VL_KL_KMAX = 1024
 VL_TOPK_KMAX = 2048
 VL_MAX_COLS = 0x7FFF0000
+VL_POLICY_ONEPASS_COLS = 245760
+VL_NORM_MAX_HS = 16384
+VL_PREF_SIGMOID, VL_PREF_IPO, VL_PREF_HINGE = 0, 1, 2
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int64
 _F = ctypes.c_float
+_C = ctypes.c_int
 
 _SIGS = {
     "vl_ce_fwd": [_P, _I, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P],
@@ -48,6 +52,19 @@ _SIGS = {
     "vl_acc_add": [_P, _P, _I, _P],
     "vl_test_inject_wait_timeout": [_I, _I],
     "vl_window_mean": [_P, _I, _I, _I, _P, _P],
+    "vl_policy_loss": [_P, _I, _I, _I, _P, _P, _P, _P, _P, _F, _F, _F, _F, _P, _I, _P, _P, _P, _P, _P, _P],
+    "vl_policy_loss_bf16": [_P, _I, _I, _I, _P, _P, _P, _P, _P, _F, _F, _F, _F, _P, _I, _P, _P, _P, _P, _P, _P],
+    "vl_preference_loss": [_P, _I, _I, _I, _P, _P, _P, _I, _P, _F, _F, _C, _F, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P],
+    "vl_preference_loss_bf16": [_P, _I, _I, _I, _P, _P, _P, _I, _P, _F, _F, _C, _F, _P, _I, _P, _P, _P, _P, _P, _P, _I,
+                                _P],
+    "vl_layernorm_fwd": [_P, _I, _I, _I, _P, _P, _F, _P, _I, _P, _P, _P],
+    "vl_layernorm_fwd_bf16": [_P, _I, _I, _I, _P, _P, _F, _P, _I, _P, _P, _P],
+    "vl_layernorm_bwd": [_P, _I, _P, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P, _I, _P],
+    "vl_layernorm_bwd_bf16": [_P, _C, _I, _P, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P, _I, _P],
+    "vl_quant_fp8_rows": [_P, _I, _I, _I, _P, _P, _P],
+    "vl_quant_fp8_rows_bf16": [_P, _I, _I, _I, _P, _P, _P],
+    "vl_quant_fp8_blocks_bf16": [_P, _I, _I, _P, _P, _P],
+    "vl_gemm_fp8_tn": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _P],
 }
 
 _lib = None
@@ -82,6 +99,10 @@ def lib() -> ctypes.CDLL:
         L.vl_teacher_topk_workspace_bytes.restype = ctypes.c_int64
         L.vl_head_kl_workspace_bytes.argtypes = [_I, _I]
         L.vl_head_kl_workspace_bytes.restype = ctypes.c_int64
+        for name in ("vl_preference_workspace_bytes", "vl_layernorm_bwd_workspace_bytes"):
+            f = getattr(L, name)
+            f.argtypes = [_I, _I]
+            f.restype = ctypes.c_int64
         _lib = L
     return _lib
 
@@ -92,7 +113,8 @@ def declared_symbols() -> list[str]:
     return sorted(set(re.findall(r"^\s*(?:[\w\s\*]+?)\b(vl_\w+)\s*\(", txt, flags=re.M)))
 
 
-_DT = {"f32": "torch.float32", "u32": "torch.uint32", "i32": "torch.int32", "bf16": "torch.bfloat16"}
+_DT = {"f32": "torch.float32", "u32": "torch.uint32", "i32": "torch.int32", "bf16": "torch.bfloat16",
+       "u8": "torch.uint8 or torch.float8_e4m3fn", "i64": "torch.int64"}
 
 
 def _ptr(x, kind: str, name: str):
@@ -106,7 +128,7 @@ def _ptr(x, kind: str, name: str):
     if not x.is_cuda:
         raise ValueError(f"{name}: tensor must live on a CUDA device")
     want = {"f32": (torch.float32,), "u32": (torch.uint32, torch.int32), "i32": (torch.int32,),
-            "bf16": (torch.bfloat16,)}[kind]
+            "bf16": (torch.bfloat16,), "u8": (torch.uint8, torch.float8_e4m3fn), "i64": (torch.int64,)}[kind]
     if x.dtype not in want:
         raise TypeError(f"{name}: dtype {x.dtype}, expected {_DT[kind]}")
     return x.data_ptr()
@@ -337,3 +359,139 @@ def vl_topk_rows_noalloc(logits, ld, ntok, V, k, loss_start, loss_end, ids, prob
     _check("vl_topk_rows_noalloc", lib().vl_topk_rows_noalloc(
         _ptr(logits, "f32", "logits"), ld, ntok, V, k, loss_start, loss_end, _ptr(ids, "u32", "ids"),
         _ptr(probs, "f32", "probs"), _ptr(err, "i32", "err"), _stream(stream)))
+
+
+# ---------------------------------------------------------------- post-training
+
+
+def _ws(workspace, need, like):
+    """(address, bytes) of a workspace argument: 'auto' (the cached buffer of `like`'s device), a
+    tensor, (address, bytes), or None."""
+    if workspace is None or need == 0:
+        return None, 0
+    return _buf(workspace, need, like)
+
+
+def _policy(name, kind, logits, ld, ntok, V, actions, old_logp, ref_logp, adv, weight, clip_lo, clip_hi, kl_coef, scale,
+            grad, ldg, loss, logp, kl, total, err, stream):
+    _check(name, getattr(lib(), name)(
+        _ptr(logits, kind, "logits"), ld, ntok, V, _ptr(actions, "u32", "actions"), _ptr(old_logp, "f32", "old_logp"),
+        _ptr(ref_logp, "f32", "ref_logp"), _ptr(adv, "f32", "adv"), _ptr(weight, "f32", "weight"), clip_lo, clip_hi,
+        kl_coef, scale, _ptr(grad, kind, "grad"), ldg, _ptr(loss, "f32", "loss"), _ptr(logp, "f32", "logp"),
+        _ptr(kl, "f32", "kl"), _ptr(total, "f32", "total"), _ptr(err, "i32", "err"), _stream(stream)))
+
+
+def vl_policy_loss(logits, ld, ntok, V, actions, old_logp, ref_logp, adv, weight, clip_lo, clip_hi, kl_coef, scale, grad,
+                   ldg, loss, logp=None, kl=None, total=None, err=None, stream=None):
+    """The clipped policy loss with a KL term and the gradient of the logits (grad may be logits)."""
+    _policy("vl_policy_loss", "f32", logits, ld, ntok, V, actions, old_logp, ref_logp, adv, weight, clip_lo, clip_hi,
+            kl_coef, scale, grad, ldg, loss, logp, kl, total, err, stream)
+
+
+def vl_policy_loss_bf16(logits, ld, ntok, V, actions, old_logp, ref_logp, adv, weight, clip_lo, clip_hi, kl_coef, scale,
+                        grad, ldg, loss, logp=None, kl=None, total=None, err=None, stream=None):
+    _policy("vl_policy_loss_bf16", "bf16", logits, ld, ntok, V, actions, old_logp, ref_logp, adv, weight, clip_lo, clip_hi,
+            kl_coef, scale, grad, ldg, loss, logp, kl, total, err, stream)
+
+
+def vl_preference_workspace_bytes(ntok, npairs) -> int:
+    return int(lib().vl_preference_workspace_bytes(ntok, npairs))
+
+
+def _preference(name, dt, logits, ld, ntok, V, labels, weight, seq_start, npairs, ref_logp, beta, smooth, kind, scale, grad,
+                ldg, loss, margin, seq_logp, mean, err, workspace, stream):
+    ws, nb = _ws(workspace, vl_preference_workspace_bytes(ntok, npairs), logits)
+    _check(name, getattr(lib(), name)(
+        _ptr(logits, dt, "logits"), ld, ntok, V, _ptr(labels, "u32", "labels"), _ptr(weight, "f32", "weight"),
+        _ptr(seq_start, "i64", "seq_start"), npairs, _ptr(ref_logp, "f32", "ref_logp"), beta, smooth, kind, scale,
+        _ptr(grad, dt, "grad"), ldg, _ptr(loss, "f32", "loss"), _ptr(margin, "f32", "margin"),
+        _ptr(seq_logp, "f32", "seq_logp"), _ptr(mean, "f32", "mean"), _ptr(err, "i32", "err"), ws, nb, _stream(stream)))
+
+
+def vl_preference_loss(logits, ld, ntok, V, labels, weight, seq_start, npairs, ref_logp, beta, smooth, kind, scale, grad,
+                       ldg, loss, margin, seq_logp=None, mean=None, err=None, workspace="auto", stream=None):
+    """The preference loss over pairs of sequences and the gradient of the logits.  workspace:
+    'auto' (a cached buffer), a tensor or (address, bytes)."""
+    _preference("vl_preference_loss", "f32", logits, ld, ntok, V, labels, weight, seq_start, npairs, ref_logp, beta,
+                smooth, kind, scale, grad, ldg, loss, margin, seq_logp, mean, err, workspace, stream)
+
+
+def vl_preference_loss_bf16(logits, ld, ntok, V, labels, weight, seq_start, npairs, ref_logp, beta, smooth, kind, scale,
+                            grad, ldg, loss, margin, seq_logp=None, mean=None, err=None, workspace="auto", stream=None):
+    _preference("vl_preference_loss_bf16", "bf16", logits, ld, ntok, V, labels, weight, seq_start, npairs, ref_logp, beta,
+                smooth, kind, scale, grad, ldg, loss, margin, seq_logp, mean, err, workspace, stream)
+
+
+# ---------------------------------------------------------------- the layer norm before the head
+
+
+def _norm_fwd(name, dt, x, ldx, rows, hs, gamma, beta, eps, y, ldy, mu, rstd, stream):
+    _check(name, getattr(lib(), name)(
+        _ptr(x, dt, "x"), ldx, rows, hs, _ptr(gamma, "f32", "gamma"), _ptr(beta, "f32", "beta"), eps, _ptr(y, dt, "y"), ldy,
+        _ptr(mu, "f32", "mu"), _ptr(rstd, "f32", "rstd"), _stream(stream)))
+
+
+def vl_layernorm_fwd(x, ldx, rows, hs, gamma, beta, eps, y, ldy, mu=None, rstd=None, stream=None):
+    _norm_fwd("vl_layernorm_fwd", "f32", x, ldx, rows, hs, gamma, beta, eps, y, ldy, mu, rstd, stream)
+
+
+def vl_layernorm_fwd_bf16(x, ldx, rows, hs, gamma, beta, eps, y, ldy, mu=None, rstd=None, stream=None):
+    _norm_fwd("vl_layernorm_fwd_bf16", "bf16", x, ldx, rows, hs, gamma, beta, eps, y, ldy, mu, rstd, stream)
+
+
+def vl_layernorm_bwd_workspace_bytes(rows, hs) -> int:
+    return int(lib().vl_layernorm_bwd_workspace_bytes(rows, hs))
+
+
+def vl_layernorm_bwd(dy, lddy, x, ldx, rows, hs, gamma, mu, rstd, dx, lddx, dgamma=None, dbeta=None, workspace="auto",
+                     stream=None):
+    """Layer norm backward, fp32.  workspace: 'auto' (a cached buffer), a tensor or (address, bytes)."""
+    ws, nb = _ws(workspace if dgamma is not None or dbeta is not None else None, vl_layernorm_bwd_workspace_bytes(rows, hs),
+                 x)
+    _check("vl_layernorm_bwd", lib().vl_layernorm_bwd(
+        _ptr(dy, "f32", "dy"), lddy, _ptr(x, "f32", "x"), ldx, rows, hs, _ptr(gamma, "f32", "gamma"), _ptr(mu, "f32", "mu"),
+        _ptr(rstd, "f32", "rstd"), _ptr(dx, "f32", "dx"), lddx, _ptr(dgamma, "f32", "dgamma"), _ptr(dbeta, "f32", "dbeta"),
+        ws, nb, _stream(stream)))
+
+
+def vl_layernorm_bwd_bf16(dy, lddy, x, ldx, rows, hs, gamma, mu, rstd, dx, lddx, dgamma=None, dbeta=None,
+                          workspace="auto", stream=None, dy_f32=None):
+    """Layer norm backward for bf16 x and dx; dy bf16 or fp32, as the tensor's dtype says (for a raw
+    address give dy_f32)."""
+    if dy_f32 is None:
+        if isinstance(dy, int):
+            raise ValueError("dy_f32: needed when dy is a raw address")
+        dy_f32 = dy is not None and str(dy.dtype) == "torch.float32"
+    ws, nb = _ws(workspace if dgamma is not None or dbeta is not None else None, vl_layernorm_bwd_workspace_bytes(rows, hs),
+                 x)
+    _check("vl_layernorm_bwd_bf16", lib().vl_layernorm_bwd_bf16(
+        _ptr(dy, "f32" if dy_f32 else "bf16", "dy"), 1 if dy_f32 else 0, lddy, _ptr(x, "bf16", "x"), ldx, rows, hs,
+        _ptr(gamma, "f32", "gamma"), _ptr(mu, "f32", "mu"), _ptr(rstd, "f32", "rstd"), _ptr(dx, "bf16", "dx"), lddx,
+        _ptr(dgamma, "f32", "dgamma"), _ptr(dbeta, "f32", "dbeta"), ws, nb, _stream(stream)))
+
+
+# ---------------------------------------------------------------- the head's product in 8 bits
+
+
+def vl_quant_fp8_rows(x, ldx, M, K, q, sa, stream=None):
+    """e4m3 values q [M][K] and scales sa [ceil(K/128)][M] of fp32 rows x, blocks of 1 x 128."""
+    _check("vl_quant_fp8_rows", lib().vl_quant_fp8_rows(_ptr(x, "f32", "x"), ldx, M, K, _ptr(q, "u8", "q"),
+                                                        _ptr(sa, "f32", "sa"), _stream(stream)))
+
+
+def vl_quant_fp8_rows_bf16(x, ldx, M, K, q, sa, stream=None):
+    _check("vl_quant_fp8_rows_bf16", lib().vl_quant_fp8_rows_bf16(_ptr(x, "bf16", "x"), ldx, M, K, _ptr(q, "u8", "q"),
+                                                                  _ptr(sa, "f32", "sa"), _stream(stream)))
+
+
+def vl_quant_fp8_blocks_bf16(w, N, K, q, sb, stream=None):
+    """e4m3 values q [N][K] and scales sb [ceil(N/128)][ceil(K/128)] of a bf16 matrix w, blocks of 128 x 128."""
+    _check("vl_quant_fp8_blocks_bf16", lib().vl_quant_fp8_blocks_bf16(_ptr(w, "bf16", "w"), N, K, _ptr(q, "u8", "q"),
+                                                                      _ptr(sb, "f32", "sb"), _stream(stream)))
+
+
+def vl_gemm_fp8_tn(A, sa, B, sb, D, M, N, K, ldd, alpha=1.0, stream=None):
+    """D[M][N] = alpha * A[M][K] . B[N][K]^T over e4m3 values with a scale for each block of 128 of K."""
+    _check("vl_gemm_fp8_tn", lib().vl_gemm_fp8_tn(
+        _ptr(A, "u8", "A"), _ptr(sa, "f32", "sa"), _ptr(B, "u8", "B"), _ptr(sb, "f32", "sb"), _ptr(D, "f32", "D"), M, N, K,
+        ldd, alpha, _stream(stream)))
