@@ -457,8 +457,8 @@ VL_API vl_status vl_layernorm_bwd_bf16(const void* dy, int dy_f32, int64_t lddy,
  * With a frozen head: logits = hidden . W^T; and dx = g . Wt^T over the transposed plane Wt
  * [hs][V], whose 128 x 128 blocks have the transposed scales.
  *
- * The quantisers: over each block, scale = max(amax, 2^-100) / 448 and q = x / scale rounded
- * to the nearest e4m3 (ties to even), both divisions in fp32.  A NaN stays NaN, an infinity
+ * The quantisers: over each block, scale = max(amax, 2^-100) * fp32(1 / 448), rounded to fp32,
+ * and q = x / scale (an fp32 division) rounded to the nearest e4m3, ties to even, at most 448.  A NaN stays NaN, an infinity
  * makes its block's values 0 or NaN with an infinite scale, so that the product is NaN.
  * vl_quant_fp8_rows (fp32 x) / _bf16: blocks of 1 x 128, x [M][ldx] -> q [M][K], sa as above.
  * vl_quant_fp8_blocks_bf16: blocks of 128 x 128, w [N][K] bf16 (contiguous) -> q [N][K], sb.

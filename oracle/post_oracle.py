@@ -125,6 +125,7 @@ _TABLE = np.array([(-1.0 if b & 0x80 else 1.0) *
                    for b in range(256)])
 _TABLE[0x7F] = _TABLE[0xFF] = np.nan
 _POS = _TABLE[:0x7F]
+_INV448 = np.float32(1) / np.float32(448)
 
 
 def e4m3_value(b):
@@ -145,7 +146,8 @@ def e4m3_byte(v):
 
 
 def quant_rows(x):
-    """(bytes [M][K], scales [ceil(K/128)][M]) of fp32 rows, both divisions rounded to fp32."""
+    """(bytes [M][K], scales [ceil(K/128)][M]) of fp32 rows: scale = amax * fp32(1/448) and
+    x / scale, each rounded to fp32, then to e4m3."""
     x = np.asarray(x, np.float32)
     M, K = x.shape
     kb = -(-K // 128)
@@ -153,7 +155,7 @@ def quant_rows(x):
     for b in range(kb):
         blk = x[:, b * 128:(b + 1) * 128]
         amax = np.fmax.reduce(np.abs(blk), axis=1)
-        s[b] = np.fmax(amax, np.float32(2.0 ** -100)) / np.float32(448)
+        s[b] = np.fmax(amax, np.float32(2.0 ** -100)) * _INV448
         with np.errstate(invalid="ignore"):
             q[:, b * 128:(b + 1) * 128] = e4m3_byte(blk / s[b][:, None])
     return q, s
@@ -167,7 +169,7 @@ def quant_blocks(w):
     for i in range(nb):
         for b in range(kb):
             blk = w[i * 128:(i + 1) * 128, b * 128:(b + 1) * 128]
-            s[i, b] = max(np.abs(blk).max(), np.float32(2.0 ** -100)) / np.float32(448)
+            s[i, b] = max(np.abs(blk).max(), np.float32(2.0 ** -100)) * _INV448
             q[i * 128:(i + 1) * 128, b * 128:(b + 1) * 128] = e4m3_byte(blk / s[i, b])
     return q, s
 

@@ -1,6 +1,6 @@
 """The 8-bit head product and its quantisers on the GPU against float64.
 
-The quantisers are bit-exact (two fp32 divisions and one rounding).  The product: e4m3 products
+The quantisers are bit-exact (an fp32 product, an fp32 division and one rounding).  The product: e4m3 products
 are exact in fp32; a block's 128 of them are summed in fp32 (any order, each step off by at most
 2^-23 of the running size), then scaled and added over the blocks, so
 |d| <= (2 * 128 + ceil(K / 128) + 8) * 2^-24 * sum |a b|.

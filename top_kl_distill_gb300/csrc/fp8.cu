@@ -26,7 +26,7 @@ namespace vl {
 namespace {
 
 constexpr int BLK = 128;                 // elements of K (and of N) that share a scale
-constexpr float kE4m3Max = 448.f;
+constexpr float kInvE4m3Max = 1.f / 448.f;   // rounded to fp32: a scale is amax times this
 constexpr float kAmaxFloor = 7.888609052210118e-31f;      // 2^-100
 
 __device__ unsigned int g_watchdog;
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(256) quant_rows(const T* __restrict__ x, long 
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = k0 + j < K ? ld_elem(x + m * ldx + k0 + j) : 0.f;
         const float amax = warp_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
-        const float s = __fdiv_rn(fmaxf(amax, kAmaxFloor), kE4m3Max);
+        const float s = __fmul_rn(fmaxf(amax, kAmaxFloor), kInvE4m3Max);
         const uint32_t w = e4m3x2(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s)) |
                            e4m3x2(__fdiv_rn(v[2], s), __fdiv_rn(v[3], s)) << 16;
 #pragma unroll
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(256) quant_blocks(const __nv_bfloat16* __restr
         if (lane == 0) red[wp] = amax;
         __syncthreads();
         for (int j = 0; j < 8; ++j) amax = fmaxf(amax, red[j]);
-        const float s = __fdiv_rn(fmaxf(amax, kAmaxFloor), kE4m3Max);
+        const float s = __fmul_rn(fmaxf(amax, kAmaxFloor), kInvE4m3Max);
         for (int r = wp; r < BLK && n0 + r < N; r += 8) {
             float v[4];
 #pragma unroll

@@ -131,6 +131,7 @@ struct PairParams {
 
 cudaError_t launch_policy(const PostParams& P, float* total, cudaStream_t st);
 cudaError_t launch_preference(const PostParams& P, const PairParams& Q, cudaStream_t st);
+unsigned int post_watchdog(bool clear);
 
 // Layer norm (norm.cu); dtype is x's (and y's, dx's).
 struct NormParams {
