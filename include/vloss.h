@@ -391,7 +391,7 @@ VL_API vl_status vl_policy_loss_bf16(const uint16_t* logits, int64_t ld, int64_t
  *     VL_PREF_IPO      loss = (gap - 1 / (2 beta))^2                  (smooth is not used)
  *     VL_PREF_HINGE    loss = max(0, 1 - h)                           (smooth is not used)
  *     grad[t][j] = scale (d loss_i / d pi_s) weight_t ([j == labels[t]] - softmax(s_t)_j)
- * (scale = 1 / npairs gives the gradient of the mean.)  Sequence sums are taken in 64 bits in
+ * (scale = 1 / npairs gives the gradient of the mean.)  Sequence sums are taken in pairs of fp32 (about 48 bits) in
  * a fixed order.
  *   labels [ntok] u32; weight [ntok] fp32; seq_start [2 npairs + 1] int64, ascending, in
  *   [0, ntok] (values outside are clamped; rows of no sequence get a zero gradient);

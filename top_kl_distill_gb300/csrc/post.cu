@@ -13,8 +13,8 @@
 // statistics meet; the gradient is then one multiplication a column by
 // -c exp(mt - m - lnS), with no second read and no second exponential.
 //
-//   long rows    (rows_ring) one persistent CTA per SM, 15 consumer warps and a producer warp:
-//                a ring of six 30 KB tiles of 1-D bulk copies runs ahead of the consumers, so
+//   long rows    (rows_ring) one persistent CTA per SM, consumer warps and a producer warp: a
+//                ring of six 30 KB tiles of 1-D bulk copies runs ahead of the consumers, so
 //                the reads go on while a row's statistics meet and its gradient is written.
 //                What a row has beyond the registers (30720 columns) stays in the ring, up to
 //                two tiles.  Longer rows, and rows too few for the SMs, are split over a cluster;
@@ -112,22 +112,14 @@ __device__ __forceinline__ void skip_row(const PostParams& P, long long r, float
     if (w != 0.f && P.err) atomicAdd(P.err, 1);
 }
 
-// Warp partials (max, sum) of n <= 32 q values: every lane gets the row's (max, sum), combined
-// in a fixed order, the same bits in every warp.
+// (max, sum) of n <= 256 partials, by one warp: every lane gets the same bits.
 __device__ __forceinline__ MaxSum combine_parts(const float2* part, int n, int lane) {
-    float2 q[4];
     float M = -FLT_MAX;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int j = lane + 32 * i;
-        q[i] = j < n ? part[j] : make_float2(-FLT_MAX, 0.f);
-        M = fmaxf(M, q[i].x);
-    }
+    for (int j = lane; j < n; j += 32) M = fmaxf(M, part[j].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float T = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) T += q[i].y * ex2((q[i].x - M) * kLog2e);
+    for (int j = lane; j < n; j += 32) T += part[j].y * ex2((part[j].x - M) * kLog2e);
     return MaxSum{M, warp_sum(T)};
 }
 
@@ -137,8 +129,8 @@ template <typename T>
 __global__ void __launch_bounds__(NT) rows_twice(const __grid_constant__ PostParams P) {
     __shared__ float2 part[NT / 32];
     const int ct = threadIdx.x, n = (int)P.V;
-    pdl_wait_primary();
     pdl_launch_dependents();
+    pdl_wait_primary();
     for (long long r = blockIdx.x; r < P.ntok; r += gridDim.x) {
         const T* x = static_cast<const T*>(P.x) + r * P.ld;
         T* g = P.g ? static_cast<T*>(P.g) + r * P.ldg : nullptr;
@@ -171,8 +163,8 @@ __global__ void __launch_bounds__(DT) rows_direct(const __grid_constant__ PostPa
     __shared__ float2 part[2][DT / 32];
     const int ct = threadIdx.x, lane = ct & 31, n = (int)P.V;
     uint32_t li = 0;
-    pdl_wait_primary();
     pdl_launch_dependents();
+    pdl_wait_primary();
     for (long long i = blockIdx.x; i < P.ntok; i += gridDim.x) {
         const long long r = MODE == kGrad ? P.ntok - 1 - i : i;       // the last rows read are still in L2
         const T* x = static_cast<const T*>(P.x) + r * P.ld;
@@ -269,7 +261,7 @@ __global__ void __launch_bounds__(DT) rows_direct(const __grid_constant__ PostPa
 
 // ---------------------------------------------------------------- long rows
 
-constexpr int CW = 15;                   // consumer warps (with the producer 16: 128 registers a thread)
+constexpr int CW = 15;                   // consumer warps (with the producer 16: up to 128 registers a thread)
 constexpr int CT = CW * 32;
 constexpr int RT = CT + 32;              // + the producer warp
 constexpr int CHT = 4;                   // 16-byte chunks of a tile per consumer thread
@@ -278,7 +270,15 @@ constexpr int SLOTS = 6;
 constexpr int REGV = 64;                 // exponentials a thread holds in registers
 constexpr int HOLD = 2;                  // tiles of a row that stay in the ring until its gradient is written
 constexpr int MAXC = 8;                  // CTAs a row
+constexpr long long kKeepBytes = 64ll << 20;   // 0: 105.6 us at 8 pairs of 32000 columns, 40 MB 105.6, 64 MB 103.2, 90 MB 103.0
 constexpr int BATCH = 32;                // rows whose token data the producer fetches at once
+constexpr int kWindow = 96;              // rows a cluster takes of one window of the rows
+static_assert(kWindow * 256 <= 64 * RT - RT, "deal(): a lane's flags of a window of 256 clusters");
+// Buffers of the warps' partials.  Warp 0 settles a row while the others go on; they get no
+// further than the ring lets them (a slot is refilled only when warp 0 too has read it), so at
+// most SLOTS rows of one tile, and over a cluster one row more.
+constexpr int NB = 8;
+static_assert(NB > SLOTS + 1, "a partial is read before its buffer comes round again");
 
 __device__ unsigned int g_watchdog;
 
@@ -329,6 +329,23 @@ __device__ __forceinline__ void unpack_pairs(uint4 r, uint64_t (&v)[Pack<T>::N /
     }
 }
 
+// 16 bytes of shared memory where `p`, else 4 words `fill`; 16 bytes to global memory where `p`.
+// Predicated instructions: a branch around each chunk would keep the chunks' latencies apart.
+__device__ __forceinline__ uint4 ld_shared_if(uint32_t addr, bool p, uint32_t fill) {
+    uint4 r = make_uint4(fill, fill, fill, fill);
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w) : "r"(addr), "r"((uint32_t)p));
+    return r;
+}
+__device__ __forceinline__ void st_global_if(void* at, uint4 v, bool p, uint64_t policy) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %6;\n\t}"
+                 :: "l"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"((uint32_t)p), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void st_global_if(void* at, uint4 v, bool p) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q st.global.v4.u32 [%0], {%1, %2, %3, %4};\n\t}"
+                 :: "l"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"((uint32_t)p) : "memory");
+}
+
 // exp(v - m) of both lanes, nm = -m twice: the difference is exact where it matters (near 0).
 __device__ __forceinline__ uint64_t exp_pair(uint64_t v, uint64_t nm, uint64_t l2e) {
     float a, b;
@@ -341,7 +358,7 @@ struct Meta {
     uint32_t a;
     float xa;                            // the picked logit (kGrad: m)
     float old;                           // (kGrad: lnS)
-    float ref, adv;
+    float ref, adv;                      // (kGrad: ref holds the picked logit)
     int live;
 };
 
@@ -349,15 +366,16 @@ struct alignas(128) RSmem {
     alignas(16) unsigned char ring[SLOTS][TILE_B];
     uint64_t full[SLOTS], empty[SLOTS];
     uint64_t mfull[2], mempty[2];
-    uint64_t xbar[2];
-    float2 xw[2][MAXC * CW];             // cluster: every warp's partial, from every rank
-    float2 part[2][16];
-    float4 row[2];                       // (m, lnS, c) of the row, from the warp that settles it
+    uint64_t pbar[NB];                   // every warp's partial of a row is in
+    float2 part[NB][MAXC * CW];          // over a cluster: from every rank
+    float4 row[2];                       // (m, lnS, c, the picked column's gradient), from the warp that settles the row
+    int picked[2];                       // the picked column, -1 where the gradient row is zero
     Meta meta[2][BATCH];
+    int list[kWindow + 1];                      // this cluster's rows of the window (from its start): the counting ones first
+    int wlive[32];
     int abort;
 };
 static_assert(sizeof(RSmem) <= 227 * 1024, "shared memory of one CTA");
-static_assert(MAXC * CW <= 128, "combine_parts takes up to 128 partials");
 // Columns of a row part that the policy pass keeps on chip (less a chunk for the split's rounding).
 template <typename T>
 constexpr int kPartCols = CT * REGV + HOLD * TILE_B / (int)sizeof(T) - 16;
@@ -386,48 +404,113 @@ __device__ __forceinline__ Part part_of(const T* x, int n, int rank, int c, int 
     return p;
 }
 
+// The rows of a window, dealt out: the rows that count first, then the others, round robin over
+// the clusters.  Dealt by row number instead, the prompts (runs of rows that cost half as much,
+// or nothing) left some CTAs 12% more work than the mean.  Every CTA makes its own list, with
+// all threads: it reads the window's weights, which L2 holds.  kGrad goes backwards, as the last
+// rows read are still in L2.
+struct Window {
+    long long w0;        // first row
+    int n, live;         // rows of this cluster's list, of which the first `live` count
+};
+
 template <int MODE>
-__device__ __forceinline__ long long row_of(const PostParams& P, long long i) {
-    return MODE == kGrad ? P.ntok - 1 - i : i;      // backwards: the last rows read are still in L2
+__device__ __forceinline__ long long window_row(const PostParams& P, const Window& W, int k) {
+    return MODE == kGrad ? P.ntok - 1 - (W.w0 + k) : W.w0 + k;
+}
+
+template <int MODE>
+__device__ Window deal(const PostParams& P, RSmem& S, long long w0, long long cid, long long ncl) {
+        if (P.ntok <= ncl) {                 // one row a cluster: taken as it is, its weight read with its data
+        if (threadIdx.x == 0) S.list[0] = (int)cid;
+        __syncthreads();
+        return Window{0, 1, 1};
+    }
+    const int n = (int)min(P.ntok - w0, ncl * kWindow);
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const int per = (n + RT - 1) / RT * 32, lo = wp * per, hi = min(n, lo + per);
+    const float* wt = MODE == kGrad ? P.coef : P.weight;
+    Window W{w0, 0, 0};
+    auto counts = [&](int k) { return k < hi && wt[window_row<MODE>(P, W, k)] != 0.f; };
+    int mine = 0;
+    uint64_t flags = 0;                  // this lane's rows lo + 32 q + lane, bit q (a window is cut to fit)
+#pragma unroll 8
+    for (int q = 0; q < per / 32; ++q) {
+        const bool f = counts(lo + 32 * q + lane);
+        flags |= (uint64_t)f << q;
+        mine += __popc(__ballot_sync(0xffffffffu, f));
+    }
+    __syncthreads();                     // everybody is done with the list before
+    if (lane == 0) S.wlive[wp] = mine;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int i = 0; i < RT / 32; ++i) {
+        before += i < wp ? S.wlive[i] : 0;
+        all += S.wlive[i];
+    }
+    for (int k = lo; k < hi; k += 32) {
+        const bool c = (flags >> ((k - lo) >> 5)) & 1u;
+        const unsigned live = __ballot_sync(0xffffffffu, c), under = (1u << lane) - 1u;
+        if (k + lane < hi) {
+            const unsigned lb = (unsigned)before + __popc(live & under);
+            const unsigned j = c ? lb : (unsigned)all + (unsigned)(k + lane) - lb;     // place among all rows
+            const unsigned q = j / (unsigned)ncl;
+            if (j - q * (unsigned)ncl == (unsigned)cid) S.list[q] = k + lane;
+        }
+        before += __popc(live);
+    }
+    __syncthreads();
+    W.n = (int)((n - cid + ncl - 1) / ncl);
+    W.live = (int)((all - cid + ncl - 1) / ncl);
+    return W;
 }
 
 template <typename T, int MODE>
-__device__ void ring_producer(const PostParams& P, RSmem& S, int rank, int c, long long cid, long long ncl) {
+__device__ bool ring_producer(const PostParams& P, RSmem& S, int rank, int c, const Window& W, uint32_t& g, uint32_t& b) {
     constexpr int TE = TILE_B / (int)sizeof(T);
     const int lane = threadIdx.x & 31, n = (int)P.V;
     const int per = (n / Pack<T>::N + c - 1) / c;
-    uint32_t g = 0;
     bool ok = true;
-    // tiles [t0, t1) of item i
-    auto issue = [&](long long i, int t0, int t1) {
-        const T* x = static_cast<const T*>(P.x) + row_of<MODE>(P, i) * P.ld;
+    // The preference loss reads its logits twice; what the gradient pass reads first, the last
+    // kKeepBytes, is kept in L2 over the rest of the traffic.
+    const uint64_t gone = l2_evict_first(), keep = l2_evict_last();
+    const long long kept = MODE == kLogp ? P.ntok - kKeepBytes / (P.V * (long long)sizeof(T)) : 0;
+    // tiles [t0, t1) of list entry k
+    auto issue = [&](int k, int t0, int t1) {
+        const long long r = window_row<MODE>(P, W, S.list[k]);
+        const T* x = static_cast<const T*>(P.x) + r * P.ld;
         const Part pt = part_of(x, n, rank, c, per);
+        const uint64_t policy = MODE == kLogp && P.g && r >= kept ? keep : gone;
         for (int t = t0; t < t1 && t * TE < pt.bn; ++t) {
             const uint32_t slot = g % SLOTS, use = g / SLOTS;
             if (use > 0 && !wait_parity<false>(&S.empty[slot], (use - 1) & 1u, &S.abort, &g_watchdog)) return false;
             const uint32_t bytes = (uint32_t)min(TE, pt.bn - t * TE) * (uint32_t)sizeof(T);
             mbar_arrive_expect_tx(&S.full[slot], bytes);
-            bulk_g2s(S.ring[slot], x + pt.b0 + t * TE, bytes, &S.full[slot]);
+            if (MODE == kPolicy) bulk_g2s(S.ring[slot], x + pt.b0 + t * TE, bytes, &S.full[slot]);
+            else bulk_g2s_hint(S.ring[slot], x + pt.b0 + t * TE, bytes, &S.full[slot], policy);
             ++g;
         }
         return true;
     };
-    // The first row's tiles go out before anything is known of it (it is read even if it does
-    // not count); they never wait, so no consumer has to have started.
-    if (lane == 0 && cid < P.ntok) issue(cid, 0, SLOTS);
-    __syncwarp();
-    for (long long b = 0; cid + b * BATCH * ncl < P.ntok; ++b) {
-        const long long i = cid + (b * BATCH + lane) * ncl;
+    // The first row's tiles go out before its token data is fetched, as many as the ring takes
+    // without a consumer's help: of a window's first tiles each slot's last use is over.
+    if (lane == 0 && W.live > 0) ok = issue(0, 0, SLOTS);
+    ok = __all_sync(0xffffffffu, ok);
+    for (int k0 = 0; k0 < W.n && ok; k0 += BATCH, ++b) {
+        const int k = k0 + lane;
         Meta m;
         m.live = 0;
-        if (i < P.ntok) {
-            const long long r = row_of<MODE>(P, i);
+        if (k < W.n) {
+            const long long r = window_row<MODE>(P, W, S.list[k]);
             m.a = P.label[r];
             if (MODE == kGrad) {
                 m.w = P.coef[r];
-                m.xa = P.stats[2 * r];
-                m.old = P.stats[2 * r + 1];
-                m.live = m.w != 0.f;
+                m.live = k < W.live && m.w != 0.f;
+                if (m.live) {
+                    m.xa = P.stats[2 * r];
+                    m.old = P.stats[2 * r + 1];
+                    if ((long long)m.a < P.V) m.ref = ld_elem(static_cast<const T*>(P.x) + r * P.ld + m.a);
+                }
             } else {
                 m.w = P.weight[r];
                 if (MODE == kPolicy) {
@@ -435,43 +518,42 @@ __device__ void ring_producer(const PostParams& P, RSmem& S, int rank, int c, lo
                     m.ref = P.ref_logp ? P.ref_logp[r] : 0.f;
                     m.adv = P.adv[r];
                 }
-                m.live = m.w != 0.f && (long long)m.a < P.V;
+                m.live = k < W.live && m.w != 0.f && (long long)m.a < P.V;
                 if (m.live) m.xa = ld_elem(static_cast<const T*>(P.x) + r * P.ld + m.a);
             }
         }
-        if (ok && b >= 2) ok = wait_parity<false>(&S.mempty[b & 1], (uint32_t)((b >> 1) - 1) & 1u, &S.abort, &g_watchdog);
+        if (b >= 2) ok = wait_parity<false>(&S.mempty[b & 1], ((b >> 1) - 1) & 1u, &S.abort, &g_watchdog);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         S.meta[b & 1][lane] = m;
-        const uint32_t live = __ballot_sync(0xffffffffu, m.live != 0);
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(&S.mfull[b & 1]);
-            for (int k = 0; k < BATCH && ok; ++k) {
-                const long long ik = cid + (b * BATCH + k) * ncl;
-                if (ik >= P.ntok) break;
-                const bool first = b == 0 && k == 0;
-                if (first || (live >> k & 1u)) ok = issue(ik, first ? SLOTS : 0, 0x7fffffff);
-            }
+            for (int j = k0; j < min(k0 + BATCH, W.live) && ok; ++j) ok = issue(j, j == 0 ? SLOTS : 0, 0x7fffffff);
         }
         ok = __all_sync(0xffffffffu, ok);
     }
-    if (lane == 0)
-        for (uint32_t gt = g > (uint32_t)SLOTS ? g - SLOTS : 0u; gt < g; ++gt)
-            wait_parity_drain(&S.full[gt % SLOTS], (gt / SLOTS) & 1u);
+    return ok;
 }
 
 template <typename T, int MODE>
-__device__ void ring_consumer(const PostParams& P, RSmem& S, int rank, int c, long long cid, long long ncl) {
+__device__ void ring_consumer(const PostParams& P, RSmem& S, int rank, int c, const Window& W, uint32_t& g,
+                              uint32_t& batch, uint32_t& nx) {
     constexpr int N = Pack<T>::N, H = N / 2;
     constexpr int TE = TILE_B / (int)sizeof(T);
-    constexpr int RTILES = REGV / (CHT * N);         // tiles a thread's registers hold: 4 fp32, 2 bf16
+    constexpr int RTILES = REGV / (CHT * N);         // policy: tiles a thread's registers hold (4 fp32, 2 bf16)
     const int ct = (int)threadIdx.x, lane = ct & 31, cw = ct >> 5, n = (int)P.V;
     const int per = (n / N + c - 1) / c;
-    const uint64_t l2e = pack2(kLog2e, kLog2e);
-    uint32_t g = 0, nx = 0, k = 0, batch = 0;
-    // chunk u of the tile in `slot`
-    auto chunk = [&](uint32_t slot, int u) { return *reinterpret_cast<const uint4*>(&S.ring[slot][16 * (u * CT + ct)]); };
+    const uint64_t l2e = pack2(kLog2e, kLog2e), first = MODE == kGrad ? l2_evict_first() : 0;
+    const bool reads_meta = MODE == kGrad || cw == 0;
+    // rows of one alignment are all cut alike
+    const bool uniform = ((P.ld * (long long)sizeof(T)) & 15) == 0;
+    Part pt = part_of(static_cast<const T*>(P.x), n, rank, c, per);
+    // chunk u of the tile in `slot`, where the row has it; -inf elsewhere
+    constexpr uint32_t kNegInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+    auto chunk = [&](uint32_t slot, int u, bool here) {
+        return ld_shared_if(smem_u32(&S.ring[slot][16 * (u * CT + ct)]), here, kNegInf);
+    };
     auto await = [&](uint32_t gt) {
         wait_parity<false>(&S.full[gt % SLOTS], (gt / SLOTS) & 1u, &S.abort, &g_watchdog);
         return gt % SLOTS;
@@ -480,117 +562,123 @@ __device__ void ring_consumer(const PostParams& P, RSmem& S, int rank, int c, lo
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.empty[slot]);
     };
-    for (long long i = cid; i < P.ntok; i += ncl) {
-        if (k == BATCH) {                            // this warp is done with the batch before
+    int next = S.list[0];
+    for (int k = 0; k < W.n; ++k) {
+        if (reads_meta && k % BATCH == 0 && k > 0) { // this warp is done with the batch before
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.mempty[batch & 1]);
-            k = 0;
             ++batch;
         }
-        if (k == 0) wait_parity<false>(&S.mfull[batch & 1], (batch >> 1) & 1u, &S.abort, &g_watchdog);
-        const Meta& mt = S.meta[batch & 1][k++];
-        const long long r = row_of<MODE>(P, i);
+        const Meta& mt = S.meta[batch & 1][k % BATCH];
+        auto meta_ready = [&] {
+            if (k % BATCH == 0) wait_parity<false>(&S.mfull[batch & 1], (batch >> 1) & 1u, &S.abort, &g_watchdog);
+        };
+        const long long r = window_row<MODE>(P, W, next);
+        next = S.list[min(k + 1, W.n - 1)];
         const T* x = static_cast<const T*>(P.x) + r * P.ld;
         T* gr = P.g ? static_cast<T*>(P.g) + r * P.ldg : nullptr;
-        const Part pt = part_of(x, n, rank, c, per);
+        if (!uniform) pt = part_of(x, n, rank, c, per);
         const int nt = (pt.bn + TE - 1) / TE, n16 = pt.bn / N;
         const bool wide = ((reinterpret_cast<uintptr_t>(gr + pt.b0)) & 15u) == 0;
         const int jht = ct < pt.hn ? ct : ct >= N && ct - N < pt.tn ? pt.t0 + ct - N : -1;
-        // chunk q of the part's body is this thread's; its gradient
-        auto store = [&](int q, uint64_t (&o)[H], float f0) {
+        // chunk q of the part's body (this thread's, where the row has it): its gradient but for the
+        // picked column
+        auto store = [&](int q, uint64_t (&o)[H]) {
             T* at = gr + pt.b0 + N * q;
-            const unsigned d = mt.a - (unsigned)(pt.b0 + N * q);
             float v[N];
 #pragma unroll
             for (int e = 0; e < H; ++e) unpack2(o[e], v[2 * e], v[2 * e + 1]);
-            if (d < (unsigned)N) {
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    if ((unsigned)e == d) v[e] += f0;
-            }
-            if (wide) {
-                *reinterpret_cast<uint4*>(at) = Pack<T>::pack(v);
-            } else {
+            if (MODE == kGrad) st_global_if(at, Pack<T>::pack(v), wide && q < n16, first);
+            else st_global_if(at, Pack<T>::pack(v), wide && q < n16);
+            if (!wide && q < n16) {
 #pragma unroll
                 for (int e = 0; e < N; ++e) st_elem(at + e, v[e]);
             }
         };
-        auto store_ht = [&](float ht, float m, float lnS, float f0) {
-            float o = f0 == 0.f ? 0.f : -f0 * ex2(((ht - m) - lnS) * kLog2e);
-            if (jht == (int)mt.a) o += f0;
-            st_elem(gr + jht, o);
+        // the head or tail column of this thread, then the picked column a, which the thread that
+        // stored its chunk rewrites with `pick`
+        auto store_rest = [&](float ht, float m, float lnS, float f0, int a, float pick) {
+            if (jht >= 0) st_elem(gr + jht, -f0 * ex2(((ht - m) - lnS) * kLog2e));
+            const int d = a - pt.b0;
+            if (a >= 0 && ((unsigned)d < (unsigned)pt.bn ? (d / N) % CT == ct : a == jht)) st_elem(gr + a, pick);
         };
-        if (!mt.live) {
-            if (i == cid) {                          // its tiles were issued: let them pass
-                for (int t = 0; t < nt; ++t, ++g) release(await(g));
-            }
+        auto store_zeros = [&] {
+            uint64_t z[H] = {};
+            for (int q = ct; q < n16; q += CT) store(q, z);
+            if (jht >= 0) st_elem(gr + jht, 0.f);
+        };
+        if (k >= W.live) {
+            if (reads_meta) meta_ready();
             if (MODE != kGrad && rank == 0 && ct == 0) skip_row<MODE>(P, r, mt.w);
-            if (MODE != kLogp && gr) {
-                uint64_t z[H] = {};
-                for (int q = ct; q < n16; q += CT) store(q, z, 0.f);
-                if (jht >= 0) st_elem(gr + jht, 0.f);
-            }
+            if (MODE != kLogp && gr) store_zeros();
             continue;
         }
         const float ht = jht >= 0 ? ld_elem(x + jht) : 0.f;
-        // the gradient of a tile that is in the ring, from the row's statistics
-        auto tile_gradient = [&](uint32_t slot, int t, float m, float lnS, float f0) {
+        if (MODE == kGrad) {
+            // the row's statistics are known: each tile turned into gradient as it lands
+            meta_ready();
+            const float m = mt.xa, lnS = mt.old, f0 = mt.w;
+            if (f0 == 0.f) {                         // (one row a cluster) no weight after all
+                for (int t = 0; t < nt; ++t, ++g) release(await(g));
+                store_zeros();
+                continue;
+            }
             const uint64_t nm = pack2(-m, -m), nl = pack2(-lnS, -lnS), f2 = pack2(-f0, -f0);
-            const int q0 = t * CHT * CT + ct;
-            uint64_t v[CHT][H];
+            for (int t = 0; t < nt; ++t, ++g) {
+                const uint32_t slot = await(g);
+                const int q0 = t * CHT * CT + ct;
+                uint64_t v[CHT][H];
 #pragma unroll
-            for (int u = 0; u < CHT; ++u)
-                if (q0 + u * CT < n16) unpack_pairs<T>(chunk(slot, u), v[u]);
-            release(slot);
+                for (int u = 0; u < CHT; ++u) unpack_pairs<T>(chunk(slot, u, q0 + u * CT < n16), v[u]);
+                release(slot);
 #pragma unroll
-            for (int u = 0; u < CHT; ++u)
-                if (q0 + u * CT < n16) {
+                for (int u = 0; u < CHT; ++u) {
 #pragma unroll
                     for (int e = 0; e < H; ++e) v[u][e] = mul2(exp_pair(add2(v[u][e], nm), nl, l2e), f2);
-                    store(q0 + u * CT, v[u], f0);
+                    store(q0 + u * CT, v[u]);
                 }
-        };
-        if (MODE == kGrad) {
-            const float m = mt.xa, lnS = mt.old, c0 = mt.w;
-            for (int t = 0; t < nt; ++t, ++g) tile_gradient(await(g), t, m, lnS, c0);
-            if (jht >= 0) store_ht(ht, m, lnS, c0);
+            }
+            store_rest(ht, m, lnS, f0, (int)mt.a, f0 - f0 * ex2(((mt.ref - m) - lnS) * kLog2e));
             continue;
         }
         MaxSum ms = ms_empty();
-        if (jht >= 0) ms.m = fmaxf(ms.m, ht);
         // tile t's exponentials against the running maximum into v, their sum into ms; absent
         // chunks of a row's last tile are skipped
         auto tile = [&](int t, uint64_t (&v)[CHT][H]) {
             const uint32_t slot = await(g + (uint32_t)t);
             const int q0 = t * CHT * CT + ct;
             float M = ms.m;
+            float mu[CHT];
 #pragma unroll
-            for (int u = 0; u < CHT; ++u)
-                if (q0 + u * CT < n16) {
-                    unpack_pairs<T>(chunk(slot, u), v[u]);
+            for (int u = 0; u < CHT; ++u) {
+                unpack_pairs<T>(chunk(slot, u, q0 + u * CT < n16), v[u]);
+                mu[u] = -FLT_MAX;
 #pragma unroll
-                    for (int e = 0; e < H; ++e) {
-                        float a, b;
-                        unpack2(v[u][e], a, b);
-                        M = max3(M, a, b);
-                    }
+                for (int e = 0; e < H; ++e) {
+                    float a, b;
+                    unpack2(v[u][e], a, b);
+                    mu[u] = max3(mu[u], a, b);
                 }
+            }
             release(slot);
+#pragma unroll
+            for (int u = 0; u < CHT; u += 2) M = max3(M, mu[u], mu[u + 1]);
             ms.s *= ex2((ms.m - M) * kLog2e);
             ms.m = M;
             const uint64_t nm = pack2(-M, -M);
-            uint64_t s[2] = {};
+            uint64_t s[CHT];
 #pragma unroll
-            for (int u = 0; u < CHT; ++u)
-                if (q0 + u * CT < n16) {
+            for (int u = 0; u < CHT; ++u) {
 #pragma unroll
-                    for (int e = 0; e < H; ++e) {
-                        v[u][e] = exp_pair(v[u][e], nm, l2e);
-                        s[e & 1] = add2(s[e & 1], v[u][e]);
-                    }
+                for (int e = 0; e < H; ++e) {
+                    v[u][e] = exp_pair(v[u][e], nm, l2e);
+                    s[u] = e == 0 ? v[u][e] : add2(s[u], v[u][e]);
                 }
+            }
+#pragma unroll
+            for (int u = 1; u < CHT; ++u) s[0] = add2(s[0], s[u]);
             float a, b;
-            unpack2(add2(s[0], s[1]), a, b);
+            unpack2(s[0], a, b);
             ms.s += a + b;
         };
         uint64_t E[MODE == kPolicy ? RTILES : 1][CHT][H];
@@ -606,27 +694,22 @@ __device__ void ring_consumer(const PostParams& P, RSmem& S, int rank, int c, lo
             for (int t = RTILES; t < nt; ++t) {
                 const uint32_t slot = await(g + (uint32_t)t);
                 const int q0 = t * CHT * CT + ct;
-                uint64_t v[H];
-                float M = ms.m;
 #pragma unroll 1
                 for (int u = 0; u < CHT && q0 + u * CT < n16; ++u) {
-                    unpack_pairs<T>(chunk(slot, u), v);
+                    uint64_t v[H];
+                    unpack_pairs<T>(chunk(slot, u, true), v);
+                    float M = ms.m;
 #pragma unroll
                     for (int e = 0; e < H; ++e) {
                         float a, b;
                         unpack2(v[e], a, b);
                         M = max3(M, a, b);
                     }
-                }
-                ms.s *= ex2((ms.m - M) * kLog2e);
-                ms.m = M;
-                const uint64_t nm = pack2(-M, -M);
-#pragma unroll 1
-                for (int u = 0; u < CHT && q0 + u * CT < n16; ++u) {
-                    unpack_pairs<T>(chunk(slot, u), v);
+                    ms.s *= ex2((ms.m - M) * kLog2e);
+                    ms.m = M;
                     uint64_t s = 0;
 #pragma unroll
-                    for (int e = 0; e < H; ++e) s = add2(s, exp_pair(v[e], nm, l2e));
+                    for (int e = 0; e < H; ++e) s = add2(s, exp_pair(v[e], pack2(-M, -M), l2e));
                     float a, b;
                     unpack2(s, a, b);
                     ms.s += a + b;
@@ -637,44 +720,49 @@ __device__ void ring_consumer(const PostParams& P, RSmem& S, int rank, int c, lo
         }
         const uint32_t g0 = g;
         g += (uint32_t)nt;
-        if (jht >= 0) ms.s += ex2((ht - ms.m) * kLog2e);
+        if (jht >= 0) ms_add(ms, ht);
         const MaxSum wm = warp_max_sum(ms);
-        // The row's statistics: every warp's partial meets in warp 0, which settles the row and
-        // hands (m, lnS, c) back.  Two buffers: a warp writes one again only after it has the
-        // outcome of the row between, for which every warp (of every rank) has sent its partial,
-        // each after it was done with this buffer.
-        const uint32_t xb = nx & 1u, xpar = (nx >> 1) & 1u;
+        // every warp's partial (of every rank) meets in warp 0, which settles the row
+        const uint32_t pb = nx % NB, ppar = (nx / NB) & 1u, rb = nx & 1u;
         ++nx;
         if (c > 1) {
-            if (ct == 0) mbar_arrive_expect_tx(&S.xbar[xb], 8u * (uint32_t)(c * CW));
+            if (ct == 0) mbar_arrive_expect_tx(&S.pbar[pb], 8u * (uint32_t)(c * CW));
             if (lane < c)
-                st_async_f32x2(map_to_rank(&S.xw[xb][rank * CW + cw], (uint32_t)lane), wm.m, wm.s,
-                               map_to_rank(&S.xbar[xb], (uint32_t)lane));
-        } else {
-            if (lane == 0) S.part[xb][cw] = make_float2(wm.m, wm.s);
-            if (cw != 0) named_arrive(2, CT);
+                st_async_f32x2(map_to_rank(&S.part[pb][rank * CW + cw], (uint32_t)lane), wm.m, wm.s,
+                               map_to_rank(&S.pbar[pb], (uint32_t)lane));
+        } else if (lane == 0) {
+            S.part[pb][cw] = make_float2(wm.m, wm.s);
+            mbar_arrive(&S.pbar[pb]);
         }
         if (cw == 0) {
+            meta_ready();
+            const bool bad = !mt.live;               // a column past the row, or no weight after all
             MaxSum tot;
             if (c > 1) {
-                wait_parity<true>(&S.xbar[xb], xpar, &S.abort, &g_watchdog);
-                tot = combine_parts(S.xw[xb], c * CW, lane);
+                wait_parity<true>(&S.pbar[pb], ppar, &S.abort, &g_watchdog);
+                tot = combine_parts(S.part[pb], c * CW, lane);
             } else {
-                named_sync(2, CT);
-                const int l = lane & 15;
-                const float2 q = l < CW ? S.part[xb][l] : make_float2(-FLT_MAX, 0.f);
-                tot.m = warp_max(q.x);
-                tot.s = q.y * ex2((q.x - tot.m) * kLog2e);
-#pragma unroll
-                for (int off = 8; off > 0; off >>= 1) tot.s += __shfl_xor_sync(0xffffffffu, tot.s, off);
+                wait_parity<false>(&S.pbar[pb], ppar, &S.abort, &g_watchdog);
+                const float2 q = lane < CW ? S.part[pb][lane] : make_float2(-FLT_MAX, 0.f);
+                tot = warp_max_sum(MaxSum{q.x, q.y});
             }
             const float l = logf(tot.s);
-            const float f = settle_row<MODE>(P, r, mt.w, mt.old, mt.ref, mt.adv, mt.xa, tot.m, l, rank == 0 && lane == 0);
-            if (lane == 0) S.row[xb] = make_float4(tot.m, l, f, 0.f);
+            float f = 0.f;
+            if (!bad) f = settle_row<MODE>(P, r, mt.w, mt.old, mt.ref, mt.adv, mt.xa, tot.m, l, rank == 0 && lane == 0);
+            else if (rank == 0 && lane == 0) skip_row<MODE>(P, r, mt.w);
+            if (MODE == kPolicy && lane == 0) {
+                S.row[rb] = make_float4(tot.m, l, f, f - f * ex2(((mt.xa - tot.m) - l) * kLog2e));
+                S.picked[rb] = f != 0.f ? (int)mt.a : -1;
+            }
         }
-        named_sync(1, CT);
         if (MODE == kLogp) continue;
-        const float m = S.row[xb].x, lnS = S.row[xb].y, f0 = S.row[xb].z;
+        named_sync(1, CT);
+        const float m = S.row[rb].x, lnS = S.row[rb].y, f0 = S.row[rb].z;
+        if (f0 == 0.f) {                             // no gradient (whatever the logits hold)
+            for (int t = RTILES; t < nt; ++t) release((g0 + (uint32_t)t) % SLOTS);
+            if (gr) store_zeros();
+            continue;
+        }
         for (int t = RTILES; t < nt; ++t) {
             const uint32_t slot = (g0 + (uint32_t)t) % SLOTS;
             if (gr) {
@@ -683,10 +771,10 @@ __device__ void ring_consumer(const PostParams& P, RSmem& S, int rank, int c, lo
 #pragma unroll 1
                 for (int u = 0; u < CHT && q0 + u * CT < n16; ++u) {
                     uint64_t v[H];
-                    unpack_pairs<T>(chunk(slot, u), v);
+                    unpack_pairs<T>(chunk(slot, u, true), v);
 #pragma unroll
                     for (int e = 0; e < H; ++e) v[e] = mul2(exp_pair(add2(v[e], nm), nl, l2e), f2);
-                    store(q0 + u * CT, v, f0);
+                    store(q0 + u * CT, v);
                 }
             }
             release(slot);
@@ -695,18 +783,22 @@ __device__ void ring_consumer(const PostParams& P, RSmem& S, int rank, int c, lo
 #pragma unroll
         for (int t = 0; t < RTILES; ++t)
             if (t < nt) {
-                const float f = f0 == 0.f ? 0.f : -f0 * ex2(((mx[t] - m) - lnS) * kLog2e);
+                const float f = -f0 * ex2(((mx[t] - m) - lnS) * kLog2e);
                 const uint64_t f2 = pack2(f, f);
                 const int q0 = t * CHT * CT + ct;
 #pragma unroll
-                for (int u = 0; u < CHT; ++u)
-                    if (q0 + u * CT < n16) {
+                for (int u = 0; u < CHT; ++u) {
 #pragma unroll
-                        for (int e = 0; e < H; ++e) E[MODE == kPolicy ? t : 0][u][e] = mul2(E[MODE == kPolicy ? t : 0][u][e], f2);
-                        store(q0 + u * CT, E[MODE == kPolicy ? t : 0][u], f0);
-                    }
+                    for (int e = 0; e < H; ++e) E[MODE == kPolicy ? t : 0][u][e] = mul2(E[MODE == kPolicy ? t : 0][u][e], f2);
+                    store(q0 + u * CT, E[MODE == kPolicy ? t : 0][u]);
+                }
             }
-        if (jht >= 0) store_ht(ht, m, lnS, f0);
+        store_rest(ht, m, lnS, f0, S.picked[rb], S.row[rb].w);
+    }
+    if (reads_meta) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.mempty[batch & 1]);
+        ++batch;
     }
 }
 
@@ -723,68 +815,119 @@ __global__ void __launch_bounds__(RT, 1) rows_ring(const __grid_constant__ PostP
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&S.mfull[b], 1);
-            mbar_init(&S.mempty[b], CW);
-            mbar_init(&S.xbar[b], 1);
+            mbar_init(&S.mempty[b], MODE == kGrad ? CW : 1);
         }
+        for (int b = 0; b < NB; ++b) mbar_init(&S.pbar[b], c > 1 ? 1 : CW);
         S.abort = 0;
         fence_mbar_init_cluster();
     }
     if (c > 1) cluster_sync_all();
     else __syncthreads();
-    pdl_wait_primary();
     pdl_launch_dependents();
-    if (threadIdx.x >= CT) ring_producer<T, MODE>(P, S, rank, c, cid, ncl);
-    else ring_consumer<T, MODE>(P, S, rank, c, cid, ncl);
+    pdl_wait_primary();
+    uint32_t g = 0, batch = 0, nx = 0;
+    bool ok = true;
+    for (long long w0 = 0; w0 < P.ntok; w0 += ncl * kWindow) {
+        const Window W = deal<MODE>(P, S, w0, cid, ncl);
+        if (W.n == 0) continue;
+        if (threadIdx.x < CT) ring_consumer<T, MODE>(P, S, rank, c, W, g, batch, nx);
+        else if (ok) ok = ring_producer<T, MODE>(P, S, rank, c, W, g, batch);
+    }
+    if (threadIdx.x == CT)            // every copy issued has landed before the CTA leaves
+        for (uint32_t gt = g > (uint32_t)SLOTS ? g - SLOTS : 0u; gt < g; ++gt)
+            wait_parity_drain(&S.full[gt % SLOTS], (gt / SLOTS) & 1u);
     __syncwarp();
     if (c > 1) cluster_sync_all();       // no CTA may leave while a peer can still write to it
 }
 
 // ---------------------------------------------------------------- pairs
 
-// One CTA a pair: both sequences' sums in 64 bits, the pair's loss, and each row's factor.
-constexpr int PT = 256;
+// Unevaluated pairs of floats (about 48 bits): the sums over a sequence and over the rows. The
+// card's 64-bit rate is far below its 32-bit one (the pair kernel took 11 us with doubles).
+struct FF {
+    float hi, lo;
+};
+__device__ __forceinline__ FF two_sum(float a, float b) {
+    const float s = a + b, bb = s - a;
+    return FF{s, (a - (s - bb)) + (b - bb)};
+}
+__device__ __forceinline__ FF ff_add(FF a, FF b) {
+    const FF s = two_sum(a.hi, b.hi);
+    // an infinite or NaN sum has no error term (inf - inf would make one)
+    const float e = isfinite(s.hi) ? s.lo + (a.lo + b.lo) : 0.f;
+    const float h = s.hi + e;
+    return FF{h, isfinite(h) ? e - (h - s.hi) : 0.f};
+}
+__device__ __forceinline__ FF ff_mul(float a, float b) {
+    const float p = a * b;
+    return FF{p, isfinite(p) ? fmaf(a, b, -p) : 0.f};
+}
 
-__device__ double cta_sum(double v, double* red) {
-    const int t = threadIdx.x;
-    red[t] = v;
+__device__ __forceinline__ FF warp_sum_ff(FF v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        v = ff_add(v, FF{__shfl_xor_sync(0xffffffffu, v.hi, off), __shfl_xor_sync(0xffffffffu, v.lo, off)});
+    return v;
+}
+
+// The sum over the CTA's 1024 threads, in a fixed order; every thread gets it.
+__device__ FF cta_sum(FF v, FF* red) {
+    v = warp_sum_ff(v);
     __syncthreads();
-    for (int off = PT / 2; off > 0; off >>= 1) {
-        if (t < off) red[t] += red[t + off];
-        __syncthreads();
-    }
-    const double s = red[0];
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    return s;
+    return warp_sum_ff(red[threadIdx.x & 31]);
 }
 
 __device__ __forceinline__ float softplus(float v) {       // ln(1 + e^v)
     return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
 }
 
-__global__ void __launch_bounds__(PT) pair_kernel(const __grid_constant__ PairParams Q) {
-    __shared__ double red[PT];
-    pdl_wait_primary();
+// The pairs, in one launch of one cluster, so that the mean needs no other: each group of 128
+// threads takes pairs group, group + 64, ...: both sequences' sums, the pair's loss and each row's
+// factor.  After the cluster's barrier one CTA sums the losses.
+constexpr int kPairCtas = 8, kPairGroups = 8, GTH = 1024 / kPairGroups;
+
+__global__ void __cluster_dims__(kPairCtas, 1, 1) __launch_bounds__(1024) pair_kernel(const __grid_constant__ PairParams Q) {
+    __shared__ FF red[32];
+    __shared__ FF part[kPairGroups][2][GTH / 32];
+    __shared__ int flag[kPairGroups][GTH / 32];
+    const int grp = threadIdx.x / GTH, gt = threadIdx.x % GTH, lane = threadIdx.x & 31, gw = gt >> 5;
     pdl_launch_dependents();
-    for (long long i = blockIdx.x; i < Q.npairs; i += gridDim.x) {
+    pdl_wait_primary();
+    for (long long i = blockIdx.x * kPairGroups + grp; i < Q.npairs; i += kPairCtas * kPairGroups) {
         long long lo[2], hi[2];
-        double sum[2];
         int bad = 0;
         for (int k = 0; k < 2; ++k) {
             const long long s = i + (k ? Q.npairs : 0);
             lo[k] = min(max(Q.start[s], 0ll), Q.ntok);
             hi[k] = min(max(Q.start[s + 1], lo[k]), Q.ntok);
-            double v = 0.0;
-            for (long long t = lo[k] + threadIdx.x; t < hi[k]; t += PT) {
-                const float w = Q.weight[t];
-                if (w == 0.f) continue;
-                if (signbit(Q.coef[t])) bad = 1;
-                v += (double)w * (double)Q.logp[t];
-            }
-            sum[k] = cta_sum(v, red);
         }
-        bad = __syncthreads_or(bad);
-        const double gap = (sum[0] - (Q.ref ? (double)Q.ref[i] : 0.0)) - (sum[1] - (Q.ref ? (double)Q.ref[Q.npairs + i] : 0.0));
-        const float h = (float)((double)Q.beta * gap);
+        for (int k = 0; k < 2; ++k) {
+            FF v{0.f, 0.f};
+#pragma unroll 4
+            for (long long t = lo[k] + gt; t < hi[k]; t += GTH) {
+                const float w = Q.weight[t], c = Q.coef[t], l = Q.logp[t];
+                if (w == 0.f) continue;
+                if (signbit(c)) bad = 1;
+                v = ff_add(v, ff_mul(w, l));
+            }
+            v = warp_sum_ff(v);
+            if (lane == 0) part[grp][k][gw] = v;
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) flag[grp][gw] = bad;
+        named_sync(1 + grp, GTH);
+        FF sum[2];
+        for (int k = 0; k < 2; ++k) {
+            sum[k] = part[grp][k][0];
+            for (int j = 1; j < GTH / 32; ++j) sum[k] = ff_add(sum[k], part[grp][k][j]);
+        }
+        bad = 0;
+        for (int j = 0; j < GTH / 32; ++j) bad |= flag[grp][j];
+        FF gap = ff_add(sum[0], FF{-sum[1].hi, -sum[1].lo});
+        if (Q.ref) gap = ff_add(gap, two_sum(-Q.ref[i], Q.ref[Q.npairs + i]));
+        const float h = Q.beta * gap.hi + Q.beta * gap.lo;
         float loss, d;                              // d loss / d gap
         if (Q.kind == VL_PREF_SIGMOID) {
             loss = (1.f - Q.smooth) * softplus(-h) + Q.smooth * softplus(h);
@@ -792,45 +935,48 @@ __global__ void __launch_bounds__(PT) pair_kernel(const __grid_constant__ PairPa
             const float e = expf(-fabsf(h)), small = e / (1.f + e);
             d = Q.beta * (h >= 0.f ? Q.smooth - small : small - (1.f - Q.smooth));
         } else if (Q.kind == VL_PREF_IPO) {
-            const float z = (float)(gap - 0.5 / (double)Q.beta);
+            const float half = 0.5f / Q.beta, rest = fmaf(-half, Q.beta, 0.5f) / Q.beta;    // 1 / (2 beta), in two parts
+            const FF zz = ff_add(gap, FF{-half, -rest});
+            const float z = zz.hi + zz.lo;
             loss = z * z;
             d = 2.f * z;
         } else {
             loss = h < 1.f ? 1.f - h : h >= 1.f ? 0.f : h;    // a NaN stays one
             d = h < 1.f ? -Q.beta : h >= 1.f ? 0.f : h;
         }
-        if (threadIdx.x == 0) {
+        if (gt == 0) {
             Q.loss[i] = loss;
             Q.margin[i] = h;
             if (Q.seq) {
-                Q.seq[i] = (float)sum[0];
-                Q.seq[Q.npairs + i] = (float)sum[1];
+                Q.seq[i] = sum[0].hi + sum[0].lo;
+                Q.seq[Q.npairs + i] = sum[1].hi + sum[1].lo;
             }
         }
         for (int k = 0; k < 2; ++k)
-            for (long long t = lo[k] + threadIdx.x; t < hi[k]; t += PT) {
+            for (long long t = lo[k] + gt; t < hi[k]; t += GTH) {
                 const float w = Q.weight[t];
                 Q.coef[t] = bad || w == 0.f ? 0.f : Q.scale * (k ? -d : d) * w;
             }
-        __syncthreads();
+        named_sync(1 + grp, GTH);                   // the partials' buffer is free again
     }
+    if (!Q.mean) return;
+    cluster_sync_all();                             // every loss is written, visible to the cluster
+    if (blockIdx.x != 0) return;
+    FF v{0.f, 0.f};
+    for (long long i = threadIdx.x; i < Q.npairs; i += 1024) v = ff_add(v, FF{__ldcg(Q.loss + i), 0.f});
+    v = cta_sum(v, red);
+    if (threadIdx.x == 0) *Q.mean = Q.npairs > 0 ? v.hi / (float)Q.npairs + v.lo / (float)Q.npairs : 0.f;
 }
 
-// The sum of n losses, in 64 bits and a fixed order.
+// The sum of n losses.
 __global__ void __launch_bounds__(1024) total_kernel(const float* loss, long long n, float* total) {
-    __shared__ double red[32];
-    pdl_wait_primary();
+    __shared__ FF red[32];
     pdl_launch_dependents();
-    double v = 0.0;
-    for (long long i = threadIdx.x; i < n; i += 1024) v += (double)loss[i];
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        v = red[threadIdx.x];
-        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-        if (threadIdx.x == 0) *total = (float)v;
-    }
+    pdl_wait_primary();
+    FF v{0.f, 0.f};
+    for (long long i = threadIdx.x; i < n; i += 1024) v = ff_add(v, FF{loss[i], 0.f});
+    v = cta_sum(v, red);
+    if (threadIdx.x == 0) *total = v.hi + v.lo;
 }
 
 template <typename K, typename... Args>
@@ -867,7 +1013,7 @@ int ring_clusters(int dev, int c) {
     v = sms;
     if (c > 1) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(c * sms), 1, 1);
+        cfg.gridDim = dim3((unsigned)(c * v), 1, 1);
         cfg.blockDim = dim3(RT, 1, 1);
         cfg.dynamicSmemBytes = sizeof(RSmem);
         cudaLaunchAttribute attr[1];
@@ -950,8 +1096,7 @@ cudaError_t launch_policy(const PostParams& P, float* total, cudaStream_t st) {
 cudaError_t launch_preference(const PostParams& P, const PairParams& Q, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     if (P.ntok > 0) e = launch_post<kLogp>(P, st);
-    if (e == cudaSuccess && Q.npairs > 0)
-        e = launch_pdl(pair_kernel, Q.npairs < 65536 ? Q.npairs : 65536, PT, st, Q);
+    if (e == cudaSuccess) e = launch_pdl(pair_kernel, kPairCtas, 1024, st, Q);
     if (e == cudaSuccess && P.ntok > 0 && P.g) e = launch_post<kGrad>(P, st);
     return e;
 }

@@ -148,8 +148,8 @@ vl_status preference_impl(const char* fn, const void* logits, int dtype, int64_t
     Q.loss = loss;
     Q.margin = margin;
     Q.seq = seq_logp;
-    cudaError_t e = launch_preference(P, Q, as_stream(stream));
-    if (e == cudaSuccess && mean) e = launch_mean(loss, 0, npairs, mean, as_stream(stream));
+    Q.mean = mean;
+    const cudaError_t e = launch_preference(P, Q, as_stream(stream));
     return e == cudaSuccess ? VL_OK : cuda_fail(e, fn);
 }
 

@@ -16,8 +16,4 @@ int num_sms();
 
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
-// *mean = sum of loss[ls, le) / (le - ls), 0 for an empty window, launched as a programmatic
-// dependent of the kernel that writes the losses.
-cudaError_t launch_mean(const float* loss, long long ls, long long le, float* mean, cudaStream_t st);
-
 }  // namespace vl

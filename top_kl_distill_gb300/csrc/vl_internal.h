@@ -127,6 +127,7 @@ struct PairParams {
     float* loss;
     float* margin;
     float* seq;               // nullable
+    float* mean;              // nullable
 };
 
 cudaError_t launch_policy(const PostParams& P, float* total, cudaStream_t st);

@@ -221,8 +221,6 @@ __global__ void __launch_bounds__(1024) mean_kernel(const float* __restrict__ lo
     }
 }
 
-}  // namespace
-
 cudaError_t launch_mean(const float* loss, long long ls, long long le, float* mean, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, 1);
@@ -236,8 +234,6 @@ cudaError_t launch_mean(const float* loss, long long ls, long long le, float* me
     void* args[] = {(void*)&loss, (void*)&ls, (void*)&le, (void*)&mean};
     return cudaLaunchKernelExC(&cfg, (const void*)mean_kernel, args);
 }
-
-namespace {
 
 RowParams base_params(const void* logits, int dtype, int64_t ld, int64_t ntok, int64_t V) {
     RowParams P;
