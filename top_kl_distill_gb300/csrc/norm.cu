@@ -6,23 +6,28 @@
 //
 // HBM bound: forward reads x and writes y, backward reads x and dy and writes dx, each once.
 //
-// Forward: a group of T threads holds a row, as it lies in memory, in registers (up to 128 bytes
-// a thread, so that one or two warps hold a row and its two sums cost little): the mean, then the
-// squared deviations from it (no cancellation for rows far from zero), then y.  Many small CTAs an
-// SM overlap one another's loads, sums and stores.  Calls with few rows spread a row over more
-// threads instead.
+// One persistent CTA per SM; a row belongs to a group of T threads, 16 (or 32) elements a thread,
+// several groups a CTA.  A group's rows are fetched ahead of it by 1-D bulk copies (TMA) into its
+// ring in shared memory, a row a stage: one copy of each operand, issued by one thread.  (With a
+// cp.async per 16 bytes and thread instead, issuing the copies was half of the backward pass's
+// time.)  A row is read from its stage once, so the group's own sum, whose barrier every thread
+// passes after reading, is what frees the stage.  Backward threads keep their columns over all
+// rows: gamma stays in registers, and dgamma and dbeta build up there; forward keeps gamma and beta
+// in shared memory (from the caches, which the ring leaves 30 KB, they took half of a row's time).  Forward takes the mean, then
+// the squared deviations from it (no cancellation for rows far from zero), each one sum over the
+// group; backward one sum of two values.  The CTAs' column sums meet in a fixed order (the
+// workspace, then one kernel over it): the same bits on every call.
 //
-// Backward: a thread keeps its columns, 8 or 16 of them, over all the rows of its (persistent,
-// one per SM) CTA, so that dgamma and dbeta build up in registers.  That leaves many threads a
-// row and long sums, so rows are fetched ahead: each thread copies its own elements of the next
-// rows into its own place in shared memory with cp.async and waits only for its own copies; no
-// barrier guards the buffers.  The row is read from there twice, around the group's one sum.
-// The CTAs' column sums meet in a fixed order (the workspace, then one kernel over it): the same
-// bits on every call.
+// Alignment: a copy covers the 16-byte blocks that hold the row, so that it starts on a 16-byte
+// boundary; where those blocks would leave the matrix (its first and last row at most) the group
+// copies the row element by element.  Threads read 16 bytes of x (8 beside an fp32 dy of a bf16
+// row) at a time where addresses, strides and hs allow it, else 2 elements, else 1.
 //
-// Vectors: 16 bytes of x a load where addresses, strides and hs allow it, else 2 elements, else 1.
+// Forward calls of few rows (norm_fwd_few) instead spread a row over more threads, one vector
+// each, straight from global memory: the shortest path through a row.
 #include "vl_device.cuh"
 #include "vl_internal.h"
+#include "vl_pair.cuh"
 #include "vl_rowio.cuh"
 #include "vloss.h"
 
@@ -31,9 +36,13 @@
 namespace vl {
 namespace {
 
-constexpr int FT = 512;                  // forward: threads of a row at most
-constexpr int BT = 1024;                 // backward: threads of a CTA
-constexpr int MAXG = 32;                 // rows a CTA works on at once
+constexpr int FEW = 512;                 // threads of a row at most, calls of few rows
+constexpr int FWD = 768, BWD = 512;      // threads of a CTA: up to 80 and 128 registers each
+constexpr int RING_B = 192 * 1024;       // shared memory for rows in flight (forward: and gamma and beta)
+constexpr int MAXD = 8;                  // rows in flight a group
+constexpr int MAXG = FWD / 32;           // groups a CTA
+
+__device__ unsigned int g_watchdog;
 
 // V elements of type T, as they lie in memory.
 template <typename T, int V>
@@ -75,6 +84,9 @@ template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
     if constexpr (V * sizeof(T) == 16) {
         *reinterpret_cast<uint4*>(p) = Pack<T>::pack(f);
+    } else if constexpr (sizeof(T) == 2 && V == 4) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+        *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     } else if constexpr (sizeof(T) == 4 && V == 2) {
         *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
     } else if constexpr (sizeof(T) == 2 && V == 2) {
@@ -93,13 +105,17 @@ __device__ __forceinline__ float2 group_sum(float2 v, float2* red, int T, int id
         v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
     }
     if (T == 32) return v;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x % T) >> 5, W = T / 32;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = T / 32;
     if (lane == 0) red[w] = v;
     named_sync((uint32_t)id, (uint32_t)T);
-    if (W == 2) return make_float2(red[0].x + red[1].x, red[0].y + red[1].y);
-    v = lane < W ? red[lane] : make_float2(0.f, 0.f);
+    if (W <= 4) {
+        v = make_float2(red[0].x + red[1].x, red[0].y + red[1].y);
+        if (W > 2) v = make_float2(v.x + red[2].x, v.y + red[2].y);
+        return W > 3 ? make_float2(v.x + red[3].x, v.y + red[3].y) : v;
+    }
+    v = (lane & 15) < W ? red[lane & 15] : make_float2(0.f, 0.f);      // W <= BWD / 32
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
+    for (int off = 8; off > 0; off >>= 1) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
         v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
     }
@@ -109,264 +125,464 @@ __device__ __forceinline__ float group_sum(float v, float2* red, int T, int id) 
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     if (T == 32) return v;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x % T) >> 5, W = T / 32;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = T / 32;
     if (lane == 0) red[w].x = v;
     named_sync((uint32_t)id, (uint32_t)T);
-    if (W == 2) return red[0].x + red[1].x;
+    if (W <= 4) {
+        v = red[0].x + red[1].x;
+        if (W > 2) v += red[2].x;
+        return W > 3 ? v + red[3].x : v;
+    }
     v = lane < W ? red[lane].x : 0.f;
 #pragma unroll
-    for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return __shfl_sync(0xffffffffu, v, 0);
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
 }
-static_assert(FT / 32 <= 16, "the forward sum's second step takes 16 lanes");
 
-// n floats of an affine vector (nullptr: `none`).
+
+// The pairs of n = U V elements a thread has of a row, element i of vector u at u V + i.
+template <typename T, int V, int U>
+__device__ __forceinline__ void to_pairs(const Vec<T, V> (&v)[U], uint64_t (&p)[U * V / 2]) {
+#pragma unroll
+    for (int k = 0; k < U * V / 2; ++k) p[k] = pack2(v[2 * k / V].get(2 * k % V), v[(2 * k + 1) / V].get((2 * k + 1) % V));
+}
+template <typename T, int V, int U>
+__device__ __forceinline__ void from_pairs(const uint64_t (&p)[U * V / 2], int u, float (&o)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = u * V + i;
+        float a, b;
+        unpack2(p[e / 2], a, b);
+        o[i] = e & 1 ? b : a;
+    }
+}
+
+// V floats of an affine vector at column j (nullptr: `none`); wide: 4 V bytes a load.
 template <int V>
-__device__ __forceinline__ void load_affine(const float* p, int j, float none, float (&f)[V]) {
+__device__ __forceinline__ void load_affine(const float* p, int j, bool wide, float none, float (&f)[V]) {
     if (!p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = none;
-    } else if (V >= 4 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p + j) + i);
-            f[4 * i] = v.x;
-            f[4 * i + 1] = v.y;
-            f[4 * i + 2] = v.z;
-            f[4 * i + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = __ldg(p + j + i);
+        return;
     }
+    if constexpr (V == 8) {
+        if (wide) {
+            asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                         : "l"(p + j));
+            return;
+        }
+    } else if constexpr (V == 4) {
+        if (wide) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p + j));
+            f[0] = v.x;
+            f[1] = v.y;
+            f[2] = v.z;
+            f[3] = v.w;
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = __ldg(p + j + i);
+}
+__device__ __forceinline__ bool wide_affine(const float* p, int V) {
+    return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(4 * V - 1)) == 0;
 }
 
-// One row a group of TH threads, U vectors of V elements a thread.
-template <typename T, int V, int U>
-__global__ void __launch_bounds__(FT) norm_fwd(const __grid_constant__ NormParams P, int TH) {
-    __shared__ float2 red[MAXG][2][FT / 32];
-    const int grp = threadIdx.x / TH, t = threadIdx.x % TH, groups = blockDim.x / TH, nv = P.hs / V;
-    const long long r = (long long)blockIdx.x * groups + grp;
+// ---------------------------------------------------------------- rows in flight
+
+// Bytes of a stage for rows of n elements: the 16-byte blocks of a row at any alignment.
+template <typename T>
+__host__ __device__ __forceinline__ int stage_bytes(int n) {
+    return ((n * (int)sizeof(T) + 15) / 16 + 1) * 16;
+}
+
+// What this thread has seen written to shared memory (a row copied by hand) comes before the bulk
+// copies it issues next.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+struct alignas(16) Bars {
+    uint64_t full[MAXG][MAXD];
+    int abort;
+};
+
+// A wait that ran out (a bug) leaves copies in flight: they land before the CTA goes.
+__device__ __forceinline__ void drain(Bars& B, int grp, int depth, uint32_t used, int t) {
+    if (t == 0 && *(volatile int*)&B.abort)
+        for (int d = 0; d < depth; ++d) wait_parity_drain(&B.full[grp][d], (used >> d) & 1u, 200000000ll);
+}
+
+// One operand of the pass: a matrix of rows of hs elements.
+template <typename T>
+struct Rows {
+    const unsigned char* p;
+    long long pitch;                                  // bytes
+    uint32_t low, lowp;                               // their low words, for offsets within a 16-byte block
+    __device__ __forceinline__ Rows(const void* q, long long ld)
+        : p(static_cast<const unsigned char*>(q)), pitch(ld * (long long)sizeof(T)),
+          low((uint32_t)reinterpret_cast<uintptr_t>(q)), lowp((uint32_t)(ld * (long long)sizeof(T))) {}
+    // where row r starts inside its stage
+    __device__ __forceinline__ uint32_t offset(long long r) const { return (low + (uint32_t)r * lowp) & 15u; }
+    // bytes of the 16-byte blocks that hold row r
+    __device__ __forceinline__ uint32_t bytes(long long r, int hs) const {
+        return (offset(r) + (uint32_t)hs * (uint32_t)sizeof(T) + 15u) & ~15u;
+    }
+    __device__ __forceinline__ void copy(long long r, int hs, unsigned char* stage, uint64_t* bar) const {
+        bulk_g2s(stage, p + r * pitch - offset(r), bytes(r, hs), bar);
+    }
+    // the group's threads copy row r themselves
+    __device__ __forceinline__ void copy_by_hand(long long r, int hs, unsigned char* stage, int t, int TH) const {
+        T* to = reinterpret_cast<T*>(stage + offset(r));
+        for (int j = t; j < hs; j += TH) to[j] = reinterpret_cast<const T*>(p + r * pitch)[j];
+    }
+};
+
+// Rows [lo, hi) whose 16-byte blocks lie inside the matrices (all but a row or two at the ends).
+struct Safe {
+    long long lo, hi;
+    __device__ __forceinline__ bool has(long long r) const { return r >= lo && r < hi; }
+};
+
+// ---------------------------------------------------------------- forward
+
+// Few rows: a row a CTA, one vector of V elements a thread.
+template <typename T, int V>
+__global__ void __launch_bounds__(FEW) norm_fwd_few(const __grid_constant__ NormParams P) {
+    __shared__ float2 red[2][FEW / 32];
+    const int t = threadIdx.x, TH = blockDim.x, nv = P.hs / V;
+    const long long r = blockIdx.x;
+    float ga[V], be[V], x[V], s = 0.f;
     pdl_launch_dependents();
     pdl_wait_primary();
-    if (r >= P.rows) return;
-    const T* x = static_cast<const T*>(P.x) + r * P.ldx + t * V;
-    Vec<T, V> raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (t + u * TH < nv) raw[u].load(x + u * TH * V);
-    float s[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        s[u] = 0.f;
-        if (t + u * TH < nv)
-#pragma unroll
-            for (int i = 0; i < V; ++i) s[u] += raw[u].get(i);
+    Vec<T, V> raw;
+    raw.zero();
+    if (t < nv) {
+        raw.load(static_cast<const T*>(P.x) + r * P.ldx + t * V);
+        load_affine<V>(P.gamma, t * V, wide_affine(P.gamma, V), 1.f, ga);
+        load_affine<V>(P.beta, t * V, wide_affine(P.beta, V), 0.f, be);
     }
 #pragma unroll
-    for (int u = 1; u < U; ++u) s[0] += s[u];
+    for (int i = 0; i < V; ++i) s += raw.get(i);
     const float inv = 1.f / (float)P.hs;
-    const float mu = group_sum(s[0], red[grp][0], TH, 1 + grp) * inv;
+    const float mu = group_sum(s, red[0], TH, 1) * inv;
+    s = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        s[u] = 0.f;
-        if (t + u * TH < nv)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = raw[u].get(i) - mu;
-                s[u] = fmaf(d, d, s[u]);
-            }
+    for (int i = 0; i < V; ++i) {
+        x[i] = t < nv ? raw.get(i) - mu : 0.f;
+        s = fmaf(x[i], x[i], s);
     }
-#pragma unroll
-    for (int u = 1; u < U; ++u) s[0] += s[u];
-    const float var = group_sum(s[0], red[grp][1], TH, 1 + grp) * inv;
-    const float rstd = 1.f / sqrtf(var + P.eps);
+    const float var = group_sum(s, red[1], TH, 1) * inv;
+    const float rstd = __frsqrt_rn(var + P.eps);
     if (t == 0) {
         if (P.mu_out) P.mu_out[r] = mu;
         if (P.rstd_out) P.rstd_out[r] = rstd;
     }
-    T* y = static_cast<T*>(P.y) + r * P.ldy + t * V;
+    if (t < nv) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (t + u * TH < nv) {
-            float o[V], ga[V], be[V];
-            load_affine<V>(P.gamma, (t + u * TH) * V, 1.f, ga);
-            load_affine<V>(P.beta, (t + u * TH) * V, 0.f, be);
+        for (int i = 0; i < V; ++i) x[i] = fmaf(x[i] * rstd, ga[i], be[i]);
+        store_vec<T, V>(static_cast<T*>(P.y) + r * P.ldy + t * V, x);
+    }
+}
+
+template <typename T, int V, int E>
+__global__ void __launch_bounds__(FWD, 1) norm_fwd(const __grid_constant__ NormParams P, int depth, Safe safe) {
+    constexpr int U = E / V, E2 = E / 2;
+    extern __shared__ __align__(128) unsigned char dyn[];     // the groups' rings; gamma, beta
+    __shared__ Bars B;
+    __shared__ float2 red[MAXG][4][FWD / 32];
+    const int grp = threadIdx.y, t = threadIdx.x, TH = blockDim.x, groups = blockDim.y, hs = P.hs, nv = hs / V;
+    const long long stride = (long long)gridDim.x * groups, r0 = (long long)blockIdx.x * groups + grp;
+    const int sb = stage_bytes<T>(hs);
+    unsigned char* const ring = dyn + (size_t)grp * depth * sb;
+    const Rows<T> X(P.x, P.ldx);
+    if (t == 0) {
+        for (int d = 0; d < depth; ++d) mbar_init(&B.full[grp][d], 1);
+        fence_mbar_init_cluster();
+    }
+    if (t == 0 && grp == 0) B.abort = 0;
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    auto fetch = [&](long long row, int st) {
+        if (!safe.has(row)) return;
+        fence_async();
+        mbar_arrive_expect_tx(&B.full[grp][st], X.bytes(row, hs));
+        X.copy(row, hs, ring + (size_t)st * sb, &B.full[grp][st]);
+    };
+    if (t == 0)
+        for (int d = 0; d < depth; ++d) fetch(r0 + d * stride, d);
+    // gamma and beta in pieces of F floats: piece q of all vectors after piece q - 1 of all, so that
+    // a warp's 16-byte reads lie side by side
+    constexpr int F = V < 4 ? V : 4;
+    float* const aff = reinterpret_cast<float*>(dyn + (size_t)groups * depth * sb);
+    for (int j = grp * TH + t; j < hs; j += groups * TH) {
+        const int at = (j % V / F * nv + j / V) * F + j % F;
+        aff[at] = P.gamma ? P.gamma[j] : 1.f;
+        aff[hs + at] = P.beta ? P.beta[j] : 0.f;
+    }
+    __syncthreads();
+    auto affine = [&](const float* a, int v, float (&f)[V]) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = fmaf((raw[u].get(i) - mu) * rstd, ga[i], be[i]);
-            store_vec<T, V>(y + u * TH * V, o);
+        for (int q = 0; q < V / F; ++q) {
+            const float* p = a + (q * nv + v) * F;
+            if constexpr (F == 4) {
+                const float4 w = *reinterpret_cast<const float4*>(p);
+                f[4 * q] = w.x;
+                f[4 * q + 1] = w.y;
+                f[4 * q + 2] = w.z;
+                f[4 * q + 3] = w.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < F; ++i) f[i] = p[i];
+            }
         }
+    };
+    const float inv = 1.f / (float)hs;
+    const bool full = nv == U * TH;                   // no vector past the row's end
+    auto tree = [](uint64_t (&s)[4]) { return sum2(add2(add2(s[0], s[1]), add2(s[2], s[3]))); };
+    int st = 0, par = 0;
+    uint32_t used = 0;                                // bit st: the phase of stage st to wait for
+    for (long long r = r0; r < P.rows; r += stride, par ^= 2) {
+        unsigned char* const stage = ring + (size_t)st * sb;
+        if (safe.has(r)) {
+            wait_parity<false>(&B.full[grp][st], (used >> st) & 1u, &B.abort, &g_watchdog);
+            used ^= 1u << st;
+        } else {
+            X.copy_by_hand(r, hs, stage, t, TH);
+            if (TH == 32) __syncwarp();
+            else named_sync(1 + grp, TH);
+        }
+        const T* x = reinterpret_cast<const T*>(stage + X.offset(r)) + t * V;
+        uint64_t p[E2];
+        {
+            Vec<T, V> raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                raw[u].zero();
+                if (t + u * TH < nv) raw[u].load(x + u * TH * V);
+            }
+            to_pairs<T, V, U>(raw, p);
+        }
+        uint64_t s[4] = {};
+#pragma unroll
+        for (int k = 0; k < E2; ++k) s[k & 3] = add2(s[k & 3], p[k]);
+        const float mu = group_sum(tree(s), red[grp][par], TH, 1 + grp) * inv;
+        if (t == 0) fetch(r + depth * stride, st);    // past the sum: every thread has read its stage
+        const uint64_t nmu = both(-mu);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] = 0;
+#pragma unroll
+        for (int k = 0; k < E2; ++k) {
+            p[k] = add2(p[k], nmu);
+            if (!full) {
+                float a, b;
+                unpack2(p[k], a, b);
+                if (t + 2 * k / V * TH >= nv) a = 0.f;
+                if (t + (2 * k + 1) / V * TH >= nv) b = 0.f;
+                p[k] = pack2(a, b);
+            }
+            s[k & 3] = fma2(p[k], p[k], s[k & 3]);
+        }
+        const float var = group_sum(tree(s), red[grp][par + 1], TH, 1 + grp) * inv;
+        const float rstd = __frsqrt_rn(var + P.eps);
+        if (t == 0) {
+            if (P.mu_out) P.mu_out[r] = mu;
+            if (P.rstd_out) P.rstd_out[r] = rstd;
+        }
+        const uint64_t rs2 = both(rstd);
+#pragma unroll
+        for (int k = 0; k < E2; ++k) p[k] = mul2(p[k], rs2);
+        T* y = static_cast<T*>(P.y) + r * P.ldy + t * V;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u * TH < nv) {
+                float o[V], ga[V], be[V];
+                affine(aff, t + u * TH, ga);
+                affine(aff + hs, t + u * TH, be);
+                from_pairs<T, V, U>(p, u, o);
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = fmaf(o[i], ga[i], be[i]);
+                store_vec<T, V>(y + u * TH * V, o);
+            }
+        st = st + 1 == depth ? 0 : st + 1;
+    }
+    drain(B, grp, depth, used, t);
 }
 
 // ---------------------------------------------------------------- backward
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
-
-// A thread's vector of V elements in shared memory: pieces of at most 16 bytes, piece q of thread
-// t at (q blockDim + t) pieces, so that a warp's accesses are contiguous.
-template <typename T, int V>
-struct Slot {
-    static constexpr int BYTES = V * (int)sizeof(T);
-    static constexpr int PIECE = BYTES < 16 ? BYTES : 16;
-    static constexpr int PIECES = BYTES / PIECE;
-    static __device__ __forceinline__ void fetch(uint32_t base, const T* src) {
-#pragma unroll
-        for (int q = 0; q < PIECES; ++q) {
-            const uint32_t dst = base + (uint32_t)((q * blockDim.x + threadIdx.x) * PIECE);
-            if constexpr (PIECE >= 4) {
-                cp_async<PIECE>(dst, reinterpret_cast<const char*>(src) + q * PIECE);
-            } else {                               // two bytes: below what cp.async copies
-                const uint16_t v = *reinterpret_cast<const uint16_t*>(src);
-                asm volatile("st.shared.u16 [%0], %1;" :: "r"(dst), "h"(v) : "memory");
-            }
-        }
-    }
-    static __device__ __forceinline__ void read(uint32_t base, Vec<T, V>& v) {
-#pragma unroll
-        for (int q = 0; q < PIECES; ++q) {
-            const uint32_t src = base + (uint32_t)((q * blockDim.x + threadIdx.x) * PIECE);
-            if constexpr (PIECE == 16)
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v.w[4 * q]), "=r"(v.w[4 * q + 1]), "=r"(v.w[4 * q + 2]), "=r"(v.w[4 * q + 3]) : "r"(src) : "memory");
-            else if constexpr (PIECE == 8)
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.w[0]), "=r"(v.w[1]) : "r"(src) : "memory");
-            else if constexpr (PIECE == 4)
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v.w[0]) : "r"(src) : "memory");
-            else {
-                uint16_t h;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(src) : "memory");
-                v.w[0] = h;
-            }
-        }
-    }
-};
-
-// Rows in flight: what 192 KB hold.
-template <typename T, typename D, int E>
-constexpr int kDepth = []() constexpr {
-    const int n = 192 * 1024 / (BT * E * (int)(sizeof(T) + sizeof(D)));
-    return n < 1 ? 1 : n > 6 ? 6 : n;
-}();
-
 template <typename T, typename D, int V, int E, bool SUMS>
-__global__ void __launch_bounds__(BT, 1) norm_bwd(const __grid_constant__ NormParams P, int TH) {
-    constexpr int U = E / V, DEPTH = kDepth<T, D, E>;
-    constexpr bool REG = E <= 8;                      // gamma in registers, else from the caches
-    extern __shared__ __align__(16) unsigned char dyn[];
-    __shared__ float2 red[MAXG][2][BT / 32];
-    __shared__ float stat[DEPTH][BT / 32][2];         // (mu, rstd) of the rows in flight, per warp
-    const int grp = threadIdx.x / TH, t = threadIdx.x % TH, groups = blockDim.x / TH, nv = P.hs / V;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long stride = (long long)gridDim.x * groups;
-    const long long r0 = (long long)blockIdx.x * groups + grp;
-    const uint32_t sx = smem_u32(dyn), xs = blockDim.x * V * (uint32_t)sizeof(T), ds = blockDim.x * V * (uint32_t)sizeof(D);
-    const uint32_t stage = U * (xs + ds);
+__global__ void __launch_bounds__(BWD, 1) norm_bwd(const __grid_constant__ NormParams P, int depth, Safe safe) {
+    constexpr int U = E / V, E2 = E / 2;
+    constexpr bool REG = E <= 16;                     // gamma and the row's values in registers; else gamma from
+                                                      // the caches and the row from shared memory again
+    extern __shared__ __align__(128) unsigned char dyn[];
+    __shared__ Bars B;
+    __shared__ float2 red[BWD / 32][2][BWD / 32];
+    const int grp = threadIdx.y, t = threadIdx.x, TH = blockDim.x, groups = blockDim.y, hs = P.hs, nv = hs / V;
+    const long long stride = (long long)gridDim.x * groups, r0 = (long long)blockIdx.x * groups + grp;
+    const int sx = stage_bytes<T>(hs), sb = sx + stage_bytes<D>(hs);
+    unsigned char* const ring = dyn + (size_t)grp * depth * sb;
+    const Rows<T> X(P.x, P.ldx);
+    const Rows<D> Y(P.dy, P.lddy);
+    if (t == 0) {
+        for (int d = 0; d < depth; ++d) mbar_init(&B.full[grp][d], 1);
+        fence_mbar_init_cluster();
+    }
+    if (t == 0 && grp == 0) B.abort = 0;
+    __syncthreads();
     pdl_launch_dependents();
     pdl_wait_primary();
     auto fetch = [&](long long row, int st) {
-        if (row < P.rows) {
-            const T* x = static_cast<const T*>(P.x) + row * P.ldx + t * V;
-            const D* dy = static_cast<const D*>(P.dy) + row * P.lddy + t * V;
-            const uint32_t b = sx + st * stage;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u * TH < nv) {
-                    Slot<T, V>::fetch(b + u * xs, x + u * TH * V);
-                    Slot<D, V>::fetch(b + U * xs + u * ds, dy + u * TH * V);
-                }
-            if (lane < 2) cp_async<4>(smem_u32(&stat[st][warp][lane]), (lane ? P.rstd : P.mu) + row);
-        }
-        cp_commit();
+        if (!safe.has(row)) return;
+        fence_async();
+        mbar_arrive_expect_tx(&B.full[grp][st], X.bytes(row, hs) + Y.bytes(row, hs));
+        X.copy(row, hs, ring + (size_t)st * sb, &B.full[grp][st]);
+        Y.copy(row, hs, ring + (size_t)st * sb + sx, &B.full[grp][st]);
     };
-    for (int d = 0; d < DEPTH; ++d) fetch(r0 + d * stride, d);
-    float ga[REG ? U : 1][V], ag[U][V], ab[U][V];
+    if (t == 0)
+        for (int d = 0; d < depth; ++d) fetch(r0 + d * stride, d);
+    float nmu = 0.f, nrs = 0.f;
+    auto stats = [&](long long row) {
+        if (row < P.rows) {
+            nmu = P.mu[row];
+            nrs = P.rstd[row];
+        }
+    };
+    stats(r0);
+    const bool wg = wide_affine(P.gamma, V);
+    uint64_t ga[REG ? E2 : 1], ag[E2], ab[E2];
+    // gamma's pairs of this thread's vectors from u0 on, as many as g takes
+    auto gamma = [&](int u0, auto& g) {
+        constexpr int N2 = sizeof(g) / 8;
+        float f[2 * N2 / V][V];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (REG) {
-            if (t + u * TH < nv) load_affine<V>(P.gamma, (t + u * TH) * V, 1.f, ga[REG ? u : 0]);
+        for (int u = 0; u < 2 * N2 / V; ++u) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[u][i] = 0.f;
+            if (t + (u0 + u) * TH < nv) load_affine<V>(P.gamma, (t + (u0 + u) * TH) * V, wg, 1.f, f[u]);
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) ag[u][i] = ab[u][i] = 0.f;
-    }
-    const float inv = 1.f / (float)P.hs;
+        for (int k = 0; k < N2; ++k) g[k] = pack2(f[2 * k / V][2 * k % V], f[(2 * k + 1) / V][(2 * k + 1) % V]);
+    };
+    if constexpr (REG) gamma(0, ga);
+#pragma unroll
+    for (int k = 0; k < E2; ++k) ag[k] = ab[k] = 0;
+    const float inv = 1.f / (float)hs;
     int st = 0, par = 0;
+    uint32_t used = 0;                                // bit st: the phase of stage st to wait for
     for (long long r = r0; r < P.rows; r += stride, par ^= 1) {
-        cp_wait<DEPTH - 1>();
-        __syncwarp();
-        const float mu = stat[st][warp][0], rs = stat[st][warp][1];
-        const uint32_t b = sx + st * stage;
-        float2 s = make_float2(0.f, 0.f);
+        unsigned char* const stage = ring + (size_t)st * sb;
+        const uint64_t nmu2 = both(-nmu), rs2 = both(nrs);
+        stats(r + stride);
+        if (safe.has(r)) {
+            wait_parity<false>(&B.full[grp][st], (used >> st) & 1u, &B.abort, &g_watchdog);
+            used ^= 1u << st;
+        } else {
+            X.copy_by_hand(r, hs, stage, t, TH);
+            Y.copy_by_hand(r, hs, stage + sx, t, TH);
+            if (TH == 32) __syncwarp();
+            else named_sync(1 + grp, TH);
+        }
+        const T* x = reinterpret_cast<const T*>(stage + X.offset(r)) + t * V;
+        const D* dy = reinterpret_cast<const D*>(stage + sx + Y.offset(r)) + t * V;
+        // xh and dy of vectors [u0, u0 + NU) of this thread (dy 0 past the row's end)
+        constexpr int NU = REG ? U : 16 / V, C2 = NU * V / 2;
+        auto row = [&](int u0, uint64_t (&xh)[C2], uint64_t (&d)[C2]) {
+            Vec<T, V> rx[NU];
+            Vec<D, V> rd[NU];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u * TH < nv) {
-                Vec<T, V> rx;
-                Vec<D, V> rd;
-                Slot<T, V>::read(b + u * xs, rx);
-                Slot<D, V>::read(b + U * xs + u * ds, rd);
-                if (!REG) load_affine<V>(P.gamma, (t + u * TH) * V, 1.f, ga[0]);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float d = rd.get(i), xh = (rx.get(i) - mu) * rs, g = d * ga[REG ? u : 0][i];
-                    if (SUMS) {
-                        ag[u][i] = fmaf(d, xh, ag[u][i]);
-                        ab[u][i] += d;
-                    }
-                    s.x += g;
-                    s.y = fmaf(g, xh, s.y);
+            for (int u = 0; u < NU; ++u) {
+                rx[u].zero();
+                rd[u].zero();
+                if (t + (u0 + u) * TH < nv) {
+                    rx[u].load(x + (u0 + u) * TH * V);
+                    rd[u].load(dy + (u0 + u) * TH * V);
                 }
             }
-        s = group_sum(s, red[grp][par], TH, 1 + grp);
-        const float a = s.x * inv, c = s.y * inv;
+            to_pairs<T, V, NU>(rx, xh);
+            to_pairs<D, V, NU>(rd, d);
+#pragma unroll
+            for (int k = 0; k < C2; ++k) xh[k] = mul2(add2(xh[k], nmu2), rs2);
+        };
+        auto scale = [&](int u0, uint64_t (&g)[C2]) {
+            if constexpr (REG) {
+#pragma unroll
+                for (int k = 0; k < C2; ++k) g[k] = mul2(g[k], ga[k]);
+            } else {
+                uint64_t gg[C2];
+                gamma(u0, gg);
+#pragma unroll
+                for (int k = 0; k < C2; ++k) g[k] = mul2(g[k], gg[k]);
+            }
+        };
+        uint64_t xh[C2], g[C2], s1[2] = {}, s2[2] = {};
+#pragma unroll
+        for (int u0 = 0; u0 < U; u0 += NU) {
+            row(u0, xh, g);
+            if (SUMS) {
+#pragma unroll
+                for (int k = 0; k < C2; ++k) {
+                    ag[u0 * V / 2 + k] = fma2(g[k], xh[k], ag[u0 * V / 2 + k]);
+                    ab[u0 * V / 2 + k] = add2(g[k], ab[u0 * V / 2 + k]);
+                }
+            }
+            scale(u0, g);
+#pragma unroll
+            for (int k = 0; k < C2; ++k) {
+                s1[k & 1] = add2(s1[k & 1], g[k]);
+                s2[k & 1] = fma2(g[k], xh[k], s2[k & 1]);
+            }
+        }
+        const float2 s = group_sum(make_float2(sum2(add2(s1[0], s1[1])), sum2(add2(s2[0], s2[1]))), red[grp][par], TH, 1 + grp);
+        if (REG && t == 0) fetch(r + depth * stride, st);     // past the sum: every thread has read its stage
+        const uint64_t na = both(-s.x * inv), nc = both(-s.y * inv);
         T* dx = static_cast<T*>(P.y) + r * P.ldy + t * V;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u * TH < nv) {
-                Vec<T, V> rx;
-                Vec<D, V> rd;
-                Slot<T, V>::read(b + u * xs, rx);
-                Slot<D, V>::read(b + U * xs + u * ds, rd);
-                if (!REG) load_affine<V>(P.gamma, (t + u * TH) * V, 1.f, ga[0]);
-                float o[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float xh = (rx.get(i) - mu) * rs;
-                    o[i] = rs * ((rd.get(i) * ga[REG ? u : 0][i] - a) - xh * c);
-                }
-                store_vec<T, V>(dx + u * TH * V, o);
+        for (int u0 = 0; u0 < U; u0 += NU) {
+            if (!REG) {
+                row(u0, xh, g);
+                scale(u0, g);
             }
-        __syncwarp();                                // the warp has read mu and rstd
-        fetch(r + DEPTH * stride, st);
-        st = st + 1 == DEPTH ? 0 : st + 1;
+#pragma unroll
+            for (int k = 0; k < C2; ++k) g[k] = mul2(fma2(xh[k], nc, add2(g[k], na)), rs2);
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+                if (t + (u0 + u) * TH < nv) {
+                    float o[V];
+                    from_pairs<T, V, NU>(g, u, o);
+                    store_vec<T, V>(dx + (u0 + u) * TH * V, o);
+                }
+        }
+        if (!REG) {
+            if (TH == 32) __syncwarp();
+            else named_sync(1 + grp, TH);
+            if (t == 0) fetch(r + depth * stride, st);
+        }
+        st = st + 1 == depth ? 0 : st + 1;
     }
-    cp_wait<0>();
+    drain(B, grp, depth, used, t);
     if (!SUMS) return;
     // the CTA's column sums: the groups' in order (in shared memory), then to the workspace
     float* const cols = reinterpret_cast<float*>(dyn);
-    float* const out = P.part + (long long)blockIdx.x * 2 * P.hs;
-    for (int g = 0; g < groups; ++g) {
+    float* const out = P.part + (long long)blockIdx.x * 2 * hs;
+    for (int k = 0; k < groups; ++k) {
         if (groups > 1) __syncthreads();
-        if (grp == g)
+        if (grp == k)
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (t + u * TH < nv)
+                if (t + u * TH < nv) {
+                    float a[V], b[V];
+                    from_pairs<T, V, U>(ag, u, a);
+                    from_pairs<T, V, U>(ab, u, b);
+                    float* to = k + 1 < groups ? cols : out;
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         const int j = (t + u * TH) * V + i;
-                        if (g > 0) {
-                            ag[u][i] += cols[j];
-                            ab[u][i] += cols[P.hs + j];
-                        }
-                        float* to = g + 1 < groups ? cols : out;
-                        to[j] = ag[u][i];
-                        to[P.hs + j] = ab[u][i];
+                        to[j] = k > 0 ? a[i] + cols[j] : a[i];
+                        to[hs + j] = k > 0 ? b[i] + cols[hs + j] : b[i];
                     }
+                }
     }
 }
 
@@ -410,10 +626,10 @@ int num_sms_dev() {
 }
 
 template <typename K, typename... Args>
-cudaError_t launch_pdl(K kernel, long long grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+cudaError_t launch_pdl(K kernel, long long grid, dim3 threads, size_t smem, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -430,11 +646,65 @@ bool aligned(const void* p, long long ld, int es, int bytes) {
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * es % bytes == 0;
 }
 
-template <typename T, int V, int U>
-cudaError_t fwd_go(const NormParams& P, cudaStream_t st) {
-    const int TH = ((P.hs + U * V - 1) / (U * V) + 31) / 32 * 32;
-    const int groups = TH >= 256 ? 1 : TH == 32 ? 8 : 256 / TH;
-    return launch_pdl(norm_fwd<T, V, U>, (P.rows + groups - 1) / groups, groups * TH, 0, st, P, TH);
+// Threads a row and rows a CTA of `threads` threads: 16 elements a thread where that fits.
+struct Shape {
+    int E, TH, groups;
+};
+
+Shape shape_of(int hs, int threads, int small) {
+    Shape s;
+    s.E = hs <= small ? 16 : 32;
+    s.TH = ((hs + s.E - 1) / s.E + 31) / 32 * 32;
+    s.groups = threads / s.TH;
+    if (s.TH > 32 && s.groups > 15) s.groups = 15;      // named barriers 1 .. 15
+    return s;
+}
+
+int depth_of(int groups, int stage, int ring) {
+    const int d = ring / (groups * stage);
+    return d < 1 ? 1 : d > MAXD ? MAXD : d;
+}
+
+// The rows of a matrix that bulk copies of whole 16-byte blocks may take.
+Safe safe_rows(const void* p, long long ld, int es, long long rows, int hs) {
+    const uintptr_t base = reinterpret_cast<uintptr_t>(p), end = base + (uintptr_t)(((rows - 1) * ld + hs) * es);
+    Safe s{0, rows};
+    while (s.lo < rows && ((base + (uintptr_t)(s.lo * ld * es)) & ~uintptr_t(15)) < base) ++s.lo;
+    while (s.hi > s.lo && ((base + (uintptr_t)(((s.hi - 1) * ld + hs) * es) + 15) & ~uintptr_t(15)) > end) --s.hi;
+    return s;
+}
+
+// The kernel may use smem bytes of shared memory: asked for when a call needs more than any before
+// it on the device.
+template <typename F>
+cudaError_t opt_in(F kernel, size_t smem, std::atomic<int> (&had)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (had[dev].load(std::memory_order_acquire) >= (int)smem) return cudaSuccess;
+    e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 24 * 1024);
+    if (e == cudaSuccess) had[dev].store(227 * 1024 - 24 * 1024, std::memory_order_release);
+    return e;
+}
+
+template <typename T, int V, int E>
+cudaError_t fwd_go(const NormParams& P, const Shape& s, cudaStream_t st) {
+    const int stage = stage_bytes<T>(P.hs), affine = (8 * P.hs + 15) / 16 * 16;
+    const int depth = depth_of(s.groups, stage, RING_B - affine);
+    const size_t smem = (size_t)s.groups * depth * stage + affine;
+    static std::atomic<int> had[64];
+    const cudaError_t e = opt_in(norm_fwd<T, V, E>, smem, had);
+    if (e != cudaSuccess) return e;
+    const long long want = (P.rows + s.groups - 1) / s.groups, sms = num_sms_dev();
+    return launch_pdl(norm_fwd<T, V, E>, want < sms ? want : sms, dim3(s.TH, s.groups), smem, st, P, depth,
+                      safe_rows(P.x, P.ldx, sizeof(T), P.rows, P.hs));
+}
+
+template <typename T, int V>
+cudaError_t fwd_e(const NormParams& P, cudaStream_t st) {
+    const Shape s = shape_of(P.hs, FWD, 512);
+    return s.E == 16 ? fwd_go<T, V, 16>(P, s, st) : fwd_go<T, V, 32>(P, s, st);
 }
 
 template <typename T>
@@ -444,60 +714,46 @@ cudaError_t fwd(const NormParams& P, cudaStream_t st) {
         return P.hs % n == 0 && aligned(P.x, P.ldx, es, n * es) && aligned(P.y, P.ldy, es, n * es);
     };
     if (ok(N)) {
-        // few rows: one vector a thread, the shortest path through a row (while 512 threads take it)
-        if (P.rows <= num_sms_dev() && P.hs <= FT * N) return fwd_go<T, N, 1>(P, st);
-        return fwd_go<T, N, 8>(P, st);
+        if (P.rows <= num_sms_dev() && P.hs <= FEW * N)
+            return launch_pdl(norm_fwd_few<T, N>, P.rows, dim3((P.hs / N + 31) / 32 * 32), 0, st, P);
+        return fwd_e<T, N>(P, st);
     }
-    if (ok(2)) return fwd_go<T, 2, 16>(P, st);
-    return fwd_go<T, 1, 32>(P, st);
-}
-
-// Threads a row and rows a CTA of the backward pass, E elements a thread.
-struct Shape {
-    int E, TH, groups;
-};
-
-Shape shape_of(int hs) {
-    Shape s;
-    s.E = hs <= 8 * BT ? 8 : 16;
-    s.TH = ((hs + s.E - 1) / s.E + 31) / 32 * 32;
-    s.groups = BT / s.TH;
-    if (s.TH > 32 && s.groups > 15) s.groups = 15;      // named barriers 1 .. 15
-    return s;
+    if (ok(2)) return fwd_e<T, 2>(P, st);
+    return fwd_e<T, 1>(P, st);
 }
 
 template <typename T, typename D, int V, int E>
 cudaError_t bwd_go(const NormParams& P, const Shape& s, cudaStream_t st) {
     const bool sums = P.dgamma || P.dbeta;
-    const int sms = num_sms_dev(), threads = s.groups * s.TH;
     long long grid = (P.rows + s.groups - 1) / s.groups;
-    if (grid > sms) grid = sms;
-    if (grid > kMaxParts) grid = kMaxParts;
-    const size_t ring = (size_t)kDepth<T, D, E> * threads * E * (sizeof(T) + sizeof(D));
-    const size_t meet = sums && s.groups > 1 ? 8 * (size_t)P.hs : 0, smem = ring > meet ? ring : meet;
-    const void* fn = sums ? (const void*)norm_bwd<T, D, V, E, true> : (const void*)norm_bwd<T, D, V, E, false>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const int sms = num_sms_dev(), most = sms < kMaxParts ? sms : kMaxParts;
+    if (grid > most) grid = most;
+    const int stage = stage_bytes<T>(P.hs) + stage_bytes<D>(P.hs), depth = depth_of(s.groups, stage, RING_B);
+    const size_t ring = (size_t)s.groups * depth * stage, meet = 8 * (size_t)P.hs, smem = ring > meet ? ring : meet;
+    static std::atomic<int> had[2][64];
+    cudaError_t e = sums ? opt_in(norm_bwd<T, D, V, E, true>, smem, had[1]) : opt_in(norm_bwd<T, D, V, E, false>, smem, had[0]);
     if (e != cudaSuccess) return e;
-    e = sums ? launch_pdl(norm_bwd<T, D, V, E, true>, grid, threads, smem, st, P, s.TH)
-             : launch_pdl(norm_bwd<T, D, V, E, false>, grid, threads, smem, st, P, s.TH);
-    if (e == cudaSuccess && sums) e = launch_pdl(norm_join, (2 * P.hs + 31) / 32, 256, 0, st, P, (int)grid);
+    const Safe a = safe_rows(P.x, P.ldx, sizeof(T), P.rows, P.hs), b = safe_rows(P.dy, P.lddy, sizeof(D), P.rows, P.hs);
+    const Safe safe{a.lo > b.lo ? a.lo : b.lo, a.hi < b.hi ? a.hi : b.hi};
+    e = sums ? launch_pdl(norm_bwd<T, D, V, E, true>, grid, dim3(s.TH, s.groups), smem, st, P, depth, safe)
+             : launch_pdl(norm_bwd<T, D, V, E, false>, grid, dim3(s.TH, s.groups), smem, st, P, depth, safe);
+    if (e == cudaSuccess && sums) e = launch_pdl(norm_join, (2 * P.hs + 31) / 32, dim3(256), 0, st, P, (int)grid);
     return e;
 }
 
 template <typename T, typename D, int V>
 cudaError_t bwd_e(const NormParams& P, cudaStream_t st) {
-    const Shape s = shape_of(P.hs);
-    return s.E == 8 ? bwd_go<T, D, V, 8>(P, s, st) : bwd_go<T, D, V, 16>(P, s, st);
+    const Shape s = shape_of(P.hs, BWD, 16 * BWD);
+    return s.E == 16 ? bwd_go<T, D, V, 16>(P, s, st) : bwd_go<T, D, V, 32>(P, s, st);
 }
 
 template <typename T, typename D>
 cudaError_t bwd(const NormParams& P, cudaStream_t st) {
-    constexpr int N = Pack<T>::N, es = sizeof(T), ds = sizeof(D);
-    if (P.rows == 0) return launch_pdl(norm_join, (2 * P.hs + 31) / 32, 256, 0, st, P, 0);
+    constexpr int N = 16 / (sizeof(T) > sizeof(D) ? sizeof(T) : sizeof(D)), es = sizeof(T), ds = sizeof(D);
+    if (P.rows == 0) return launch_pdl(norm_join, (2 * P.hs + 31) / 32, dim3(256), 0, st, P, 0);
     auto ok = [&](int n) {
-        const int db = n * ds < 16 ? n * ds : 16;
         return P.hs % n == 0 && aligned(P.x, P.ldx, es, n * es) && aligned(P.y, P.ldy, es, n * es) &&
-               aligned(P.dy, P.lddy, ds, db);
+               aligned(P.dy, P.lddy, ds, n * ds);
     };
     if (ok(N)) return bwd_e<T, D, N>(P, st);
     if (ok(2)) return bwd_e<T, D, 2>(P, st);
@@ -507,9 +763,19 @@ cudaError_t bwd(const NormParams& P, cudaStream_t st) {
 }  // namespace
 
 long long norm_bwd_ws_bytes(long long rows, long long hs) {
-    const Shape s = shape_of((int)hs);
+    const Shape s = shape_of((int)hs, BWD, 16 * BWD);
     const long long want = (rows + s.groups - 1) / s.groups;
     return (want < kMaxParts ? want : kMaxParts) * 2 * hs * 4;
+}
+
+unsigned int norm_watchdog(bool clear) {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_watchdog, sizeof(v)) != cudaSuccess) return 0xffffffffu;
+    if (clear && v) {
+        const unsigned int z = 0;
+        if (cudaMemcpyToSymbol(g_watchdog, &z, sizeof(z)) != cudaSuccess) return 0xffffffffu;
+    }
+    return v;
 }
 
 cudaError_t launch_norm_fwd(const NormParams& P, cudaStream_t st) {

@@ -158,6 +158,7 @@ struct NormParams {
 };
 long long norm_bwd_ws_bytes(long long rows, long long hs);
 cudaError_t launch_norm_fwd(const NormParams& P, cudaStream_t st);
+unsigned int norm_watchdog(bool clear);
 cudaError_t launch_norm_bwd(const NormParams& P, cudaStream_t st);
 
 // 8-bit head product (fp8.cu).

@@ -785,12 +785,12 @@ int vl_watchdog_flag(int device, int clear) {
     }
     const unsigned int a = rows_watchdog(clear != 0), b = topk_watchdog(clear != 0),
                        c = topk_stream_watchdog(clear != 0), d = gemm_watchdog(clear != 0),
-                       e = fp8_watchdog(clear != 0), f = post_watchdog(clear != 0);
+                       e = fp8_watchdog(clear != 0), f = post_watchdog(clear != 0), g = norm_watchdog(clear != 0);
     cudaSetDevice(prev);
     if (a == 0xffffffffu || b == 0xffffffffu || c == 0xffffffffu || d == 0xffffffffu ||
-        e == 0xffffffffu || f == 0xffffffffu)
+        e == 0xffffffffu || f == 0xffffffffu || g == 0xffffffffu)
         return -1;
-    return (int)((a | b | c | d | e | f) & 0x7fffffffu);
+    return (int)((a | b | c | d | e | f | g) & 0x7fffffffu);
 }
 
 }  // extern "C"

@@ -117,26 +117,43 @@ _DT = {"f32": "torch.float32", "u32": "torch.uint32", "i32": "torch.int32", "bf1
        "u8": "torch.uint8 or torch.float8_e4m3fn", "i64": "torch.int64"}
 
 
+_torch = None
+_kinds: dict = {}
+_raw_stream = None
+
+
+def _load_torch():
+    """torch, what each kind of pointer accepts, and the quick way to the current stream's handle,
+    looked up once (a call marshals up to a dozen tensors in a few microseconds)."""
+    global _torch, _raw_stream
+    import torch
+    _kinds.update(f32=(torch.float32,), u32=(torch.uint32, torch.int32), i32=(torch.int32,), bf16=(torch.bfloat16,),
+                  u8=(torch.uint8, torch.float8_e4m3fn), i64=(torch.int64,))
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _torch = torch
+    return torch
+
+
 def _ptr(x, kind: str, name: str):
     if x is None:
         return None
     if isinstance(x, int):
         return x
-    import torch
+    torch = _torch or _load_torch()
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor, an int address or None")
     if not x.is_cuda:
         raise ValueError(f"{name}: tensor must live on a CUDA device")
-    want = {"f32": (torch.float32,), "u32": (torch.uint32, torch.int32), "i32": (torch.int32,),
-            "bf16": (torch.bfloat16,), "u8": (torch.uint8, torch.float8_e4m3fn), "i64": (torch.int64,)}[kind]
-    if x.dtype not in want:
+    if x.dtype not in _kinds[kind]:
         raise TypeError(f"{name}: dtype {x.dtype}, expected {_DT[kind]}")
     return x.data_ptr()
 
 
 def _stream(s):
     if s is None:
-        import torch
+        torch = _torch or _load_torch()
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -374,7 +391,7 @@ def _ws(workspace, need, like):
 
 def _policy(name, kind, logits, ld, ntok, V, actions, old_logp, ref_logp, adv, weight, clip_lo, clip_hi, kl_coef, scale,
             grad, ldg, loss, logp, kl, total, err, stream):
-    _check(name, getattr(lib(), name)(
+    _check(name, getattr(_lib or lib(), name)(
         _ptr(logits, kind, "logits"), ld, ntok, V, _ptr(actions, "u32", "actions"), _ptr(old_logp, "f32", "old_logp"),
         _ptr(ref_logp, "f32", "ref_logp"), _ptr(adv, "f32", "adv"), _ptr(weight, "f32", "weight"), clip_lo, clip_hi,
         kl_coef, scale, _ptr(grad, kind, "grad"), ldg, _ptr(loss, "f32", "loss"), _ptr(logp, "f32", "logp"),
@@ -401,7 +418,7 @@ def vl_preference_workspace_bytes(ntok, npairs) -> int:
 def _preference(name, dt, logits, ld, ntok, V, labels, weight, seq_start, npairs, ref_logp, beta, smooth, kind, scale, grad,
                 ldg, loss, margin, seq_logp, mean, err, workspace, stream):
     ws, nb = _ws(workspace, vl_preference_workspace_bytes(ntok, npairs), logits)
-    _check(name, getattr(lib(), name)(
+    _check(name, getattr(_lib or lib(), name)(
         _ptr(logits, dt, "logits"), ld, ntok, V, _ptr(labels, "u32", "labels"), _ptr(weight, "f32", "weight"),
         _ptr(seq_start, "i64", "seq_start"), npairs, _ptr(ref_logp, "f32", "ref_logp"), beta, smooth, kind, scale,
         _ptr(grad, dt, "grad"), ldg, _ptr(loss, "f32", "loss"), _ptr(margin, "f32", "margin"),
@@ -426,7 +443,7 @@ def vl_preference_loss_bf16(logits, ld, ntok, V, labels, weight, seq_start, npai
 
 
 def _norm_fwd(name, dt, x, ldx, rows, hs, gamma, beta, eps, y, ldy, mu, rstd, stream):
-    _check(name, getattr(lib(), name)(
+    _check(name, getattr(_lib or lib(), name)(
         _ptr(x, dt, "x"), ldx, rows, hs, _ptr(gamma, "f32", "gamma"), _ptr(beta, "f32", "beta"), eps, _ptr(y, dt, "y"), ldy,
         _ptr(mu, "f32", "mu"), _ptr(rstd, "f32", "rstd"), _stream(stream)))
 
