@@ -708,6 +708,9 @@ __device__ void ring_consumer(const PostParams& P, RSmem& S, int rank, int c, co
         const uint32_t pb = nx % NB, ppar = (nx / NB) & 1u, rb = nx & 1u;
         ++nx;
         if (c > 1) {
+            // Once every partial is in, a peer may write its part of the row, in place over the picked
+            // logit: this rank's must have been fetched by then.
+            if (MODE == kPolicy && cw == 0) meta_ready();
             if (ct == 0) mbar_arrive_expect_tx(&S.pbar[pb], 8u * (uint32_t)(c * CW));
             if (lane < c)
                 st_async_f32x2(map_to_rank(&S.part[pb][rank * CW + cw], (uint32_t)lane), wm.m, wm.s,
