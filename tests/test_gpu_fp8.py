@@ -51,6 +51,36 @@ def test_quantise_rows(M, K, pad, dtype):
     assert np.array_equal(H.host(q)[:M * K].reshape(M, K), wq) and (H.host(q)[M * K:] == 0xAA).all()
 
 
+@pytest.mark.parametrize("scales", ["any", "round", "small", "large"])
+def test_quantise_near_the_middles(scales):
+    """Values a few ulps around the middles between e4m3 values, over scales of every kind (round
+    ones: within 9 ulps of a short number): the bytes are those of an fp32 division."""
+    torch = H.torch_cuda()
+    from top_kl_distill_gb300 import vloss as vl
+    M = 6000
+    g = np.random.default_rng(len(scales))
+    amax = np.float32(448) * np.exp(g.uniform(-20, 20, M)).astype(np.float32)
+    if scales == "round":
+        amax = (np.float32(448) * g.integers(8, 16, M).astype(np.float32) * np.exp2(g.integers(-20, 20, M)).astype(np.float32))
+    elif scales == "small":
+        amax = np.exp2(g.uniform(-126, -60, M)).astype(np.float32)
+    elif scales == "large":
+        amax = np.exp2(g.uniform(100, 127.9, M)).astype(np.float32)
+    amax = (amax.view(np.int32) + g.integers(-9, 10, M).astype(np.int32)).view(np.float32)
+    s = np.maximum(amax, np.float32(2.0 ** -100)) * (np.float32(1) / np.float32(448))
+    v = np.sort(np.abs(O.e4m3_value(np.arange(0x7F))))
+    mid = ((v[1:] + v[:-1]) / 2).astype(np.float32)
+    x = mid[g.integers(0, len(mid), (M, 128))] * s[:, None]
+    x = (x.view(np.int32) + g.integers(-3, 4, x.shape).astype(np.int32)).view(np.float32)
+    x = np.minimum(np.abs(x), amax[:, None]) * g.choice(np.float32([-1, 1]), x.shape)
+    x[:, 0] = amax
+    q = torch.empty(M, 128, dtype=torch.uint8, device="cuda")
+    sa = torch.empty(1, M, device="cuda")
+    vl.vl_quant_fp8_rows(torch.from_numpy(x).cuda(), 128, M, 128, q, sa)
+    wq, ws = O.quant_rows(x)
+    assert np.array_equal(H.host(sa), ws) and np.array_equal(H.host(q), wq)
+
+
 @pytest.mark.parametrize("N,K", [(1, 16), (128, 128), (129, 130), (300, 1000), (64, 2064)])
 def test_quantise_blocks(N, K):
     torch = H.torch_cuda()

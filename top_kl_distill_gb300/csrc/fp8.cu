@@ -11,11 +11,9 @@
 //   warp 0      TMA producer: boxes of 128 x 128 bytes of A and B, 128-byte swizzle, one block of
 //               K a stage, into a 6-stage ring; both CTAs' copies are counted on the leader's
 //               (rank 0) barrier;
-//   warp 1      of the leader: tcgen05.mma (kind::f8f6f4, M = 256, N = 128, K = 32; four for each
-//               half of the columns) into the buffer of the block's parity and half, once both
-//               CTAs' epilogues have handed it back; commits to both CTAs' barriers.  Halves are
-//               handed over apart, so that one half's way through the epilogue (some 1200 cycles)
-//               overlaps the other's MMAs too;
+//   warp 1      of the leader: tcgen05.mma (kind::f8f6f4, M = 256, N = 256, K = 32; four a block)
+//               into the buffer of the block's parity, once both CTAs' epilogues have handed it
+//               back; commits to both CTAs' barriers;
 //   warp 2      tensor memory;
 //   warps 4-11  the epilogue: 32 rows (tensor-memory lanes) x 128 columns a warp, so that a thread
 //               has one row and one 128-column group: one scale a block, 128 sums in registers
@@ -24,8 +22,10 @@
 //               128-byte lines at a time.
 // Rows, columns and K past the edges: the TMA fills zeros, the epilogue masks stores; warps whose
 // rows are all past M only pass the barriers.
+#include "vl_api.h"
 #include "vl_device.cuh"
 #include "vl_internal.h"
+#include "vl_launch.h"
 #include "vl_pair.cuh"
 #include "vl_rowio.cuh"
 
@@ -53,68 +53,125 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 }
 
 __device__ __forceinline__ float warp_max(float a) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-    return a;
+    float d;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(a));
+    return d;
 }
 
-// One warp a block of 1 x 128: lane l takes elements 4 l .. 4 l + 3.
-template <typename T>
+// Four consecutive elements, those before `n` (the others 0); VEC: all four in one load.
+template <bool VEC>
+__device__ __forceinline__ float4 ld4(const float* p, int n) {
+    if (VEC) return n > 0 ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
+}
+template <bool VEC>
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p, int n) {
+    if (VEC) {
+        const uint2 r = n > 0 ? *reinterpret_cast<const uint2*>(p) : make_uint2(0u, 0u);
+        return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                           __uint_as_float(r.y & 0xffff0000u));
+    }
+    return make_float4(n > 0 ? ld_elem(p) : 0.f, n > 1 ? ld_elem(p + 1) : 0.f, n > 2 ? ld_elem(p + 2) : 0.f,
+                       n > 3 ? ld_elem(p + 3) : 0.f);
+}
+__device__ __forceinline__ float amax4(float4 v) { return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))); }
+__device__ __forceinline__ float scale_of(float amax) { return __fmul_rn(fmaxf(amax, kAmaxFloor), kInvE4m3Max); }
+
+// x / s as e4m3 needs it, from inv = fl(1 / s): p = x inv and one step of Newton's on its residual
+// (exact in an fma) leaves a relative error of 2^-47 before the last rounding, so that the result
+// can differ from fl(x / s) only where x / s is that near to the middle of two floats.  What
+// matters is whether the result lies below, on or above the middle m of two e4m3 values, a
+// 5-bit number: for the 24-bit X, S of x, s that takes |X 2^k - (M 2^20 +- 1) S| <= 4 with k >= 24,
+// so S within 4 of a multiple of 2^20.  Scales like those (a margin of 8), and those whose
+// residuals leave the normal floats, divide (inv = 0).  Weights 32000 x 4096: 85 us, 118 with a
+// division an element; rows 2048 x 32000 bf16 48 and 55, fp32 53 and 58.
+__device__ __forceinline__ float reciprocal_of(float s) {
+    const bool sound = s >= 0x1p-80f && s <= 0x1p+120f && ((__float_as_uint(s) + 8u) & 0xfffffu) > 16u;
+    return sound ? __frcp_rn(s) : 0.f;
+}
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+    const float p = x * inv;
+    return fmaf(fmaf(-p, s, x), inv, p);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void st4(uint8_t* q, float4 v, float s, float inv, int n) {
+    float4 p;
+    if (inv != 0.f) p = make_float4(quotient(v.x, s, inv), quotient(v.y, s, inv), quotient(v.z, s, inv), quotient(v.w, s, inv));
+    else p = make_float4(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s), __fdiv_rn(v.z, s), __fdiv_rn(v.w, s));
+    const uint32_t w = e4m3x2(p.x, p.y) | e4m3x2(p.z, p.w) << 16;
+    if (VEC) {
+        if (n > 0) *reinterpret_cast<uint32_t*>(q) = w;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < n) q[j] = (uint8_t)(w >> (8 * j));
+}
+
+// Both quantisers are HBM bound: fp32 in and a byte out.  Where rows start on the right boundary
+// and K is a multiple of 4 (VEC) a lane moves its four elements at once, else one by one.
+//
+// One warp takes RUN blocks of 1 x 128 of a row, all loaded before the first is reduced; the
+// warps beside it take the next rows, so that a CTA's scales are neighbours.
+constexpr int RUN = 4;
+
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) quant_rows(const T* __restrict__ x, long long ldx, long long M, int K,
                                                   uint8_t* __restrict__ q, float* __restrict__ sa) {
-    pdl_wait_primary();
     pdl_launch_dependents();
+    pdl_wait_primary();
     const int nkb = (K + BLK - 1) / BLK, lane = threadIdx.x & 31;
-    const long long total = M * nkb, stride = (long long)gridDim.x * 8;
+    const long long total = M * ((nkb + RUN - 1) / RUN), stride = (long long)gridDim.x * 8;
     for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += stride) {
-        const long long m = i / nkb;
-        const int kb = (int)(i % nkb), k0 = kb * BLK + 4 * lane;
-        float v[4];
+        const long long run = total <= 0xffffffffll ? (long long)((uint32_t)i / (uint32_t)M) : i / M, m = i - run * M;
+        const int kb = (int)run * RUN, k0 = kb * BLK + 4 * lane;
+        float4 v[RUN];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = k0 + j < K ? ld_elem(x + m * ldx + k0 + j) : 0.f;
-        const float amax = warp_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
-        const float s = __fmul_rn(fmaxf(amax, kAmaxFloor), kInvE4m3Max);
-        const uint32_t w = e4m3x2(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s)) |
-                           e4m3x2(__fdiv_rn(v[2], s), __fdiv_rn(v[3], s)) << 16;
+        for (int u = 0; u < RUN; ++u) v[u] = ld4<VEC>(x + m * ldx + k0 + u * BLK, K - k0 - u * BLK);
+        // lane u works out block u's scale and its reciprocal
+        float mine = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (k0 + j < K) q[m * K + k0 + j] = (uint8_t)(w >> (8 * j));
-        if (lane == 0) sa[kb * M + m] = s;
+        for (int u = 0; u < RUN; ++u) {
+            const float a = warp_max(amax4(v[u]));
+            mine = lane == u ? a : mine;
+        }
+        mine = scale_of(mine);
+        const float minv = reciprocal_of(mine);
+        if (lane < RUN && kb + lane < nkb) sa[(kb + lane) * M + m] = mine;
+#pragma unroll
+        for (int u = 0; u < RUN; ++u)
+            st4<VEC>(q + m * K + k0 + u * BLK, v[u], __shfl_sync(0xffffffffu, mine, u), __shfl_sync(0xffffffffu, minv, u),
+                     K - k0 - u * BLK);
     }
 }
 
-// One CTA a block of 128 x 128.
+// One CTA a block of 128 x 128, 16 rows of it a warp, in registers between the two uses.
+template <bool VEC>
 __global__ void __launch_bounds__(256) quant_blocks(const __nv_bfloat16* __restrict__ w, long long N, int K,
                                                     uint8_t* __restrict__ q, float* __restrict__ sb) {
     __shared__ float red[8];
-    pdl_wait_primary();
     pdl_launch_dependents();
+    pdl_wait_primary();
     const int nkb = (K + BLK - 1) / BLK, lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const long long blocks = (N + BLK - 1) / BLK * nkb;
     for (long long i = blockIdx.x; i < blocks; i += gridDim.x) {
-        const long long n0 = i / nkb * BLK;
+        const long long n0 = i / nkb * BLK + wp;
         const int k0 = (int)(i % nkb) * BLK + 4 * lane;
+        float4 v[16];
         float amax = 0.f;
-        for (int r = wp; r < BLK && n0 + r < N; r += 8)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (k0 + j < K) amax = fmaxf(amax, fabsf(ld_elem(w + (n0 + r) * K + k0 + j)));
+        for (int r = 0; r < 16; ++r) v[r] = ld4<VEC>(w + (n0 + 8 * r) * K + k0, n0 + 8 * r < N ? K - k0 : 0);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) amax = fmaxf(amax, amax4(v[r]));
         amax = warp_max(amax);
         __syncthreads();
         if (lane == 0) red[wp] = amax;
         __syncthreads();
         for (int j = 0; j < 8; ++j) amax = fmaxf(amax, red[j]);
-        const float s = __fmul_rn(fmaxf(amax, kAmaxFloor), kInvE4m3Max);
-        for (int r = wp; r < BLK && n0 + r < N; r += 8) {
-            float v[4];
+        const float s = scale_of(amax), inv = reciprocal_of(s);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = k0 + j < K ? ld_elem(w + (n0 + r) * K + k0 + j) : 0.f;
-            const uint32_t b = e4m3x2(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s)) |
-                               e4m3x2(__fdiv_rn(v[2], s), __fdiv_rn(v[3], s)) << 16;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (k0 + j < K) q[(n0 + r) * K + k0 + j] = (uint8_t)(b >> (8 * j));
-        }
+        for (int r = 0; r < 16; ++r) st4<VEC>(q + (n0 + 8 * r) * K + k0, v[r], s, inv, n0 + 8 * r < N ? K - k0 : 0);
         if (threadIdx.x == 0) sb[i] = s;
     }
 }
@@ -666,45 +723,31 @@ bool make_map(CUtensorMap* map, const void* base, long long rows, long long K, i
 
 std::atomic<int> g_attr[64];
 
-cudaError_t device_sms(int dev, int* sms) {
-    static std::atomic<int> cache[64];
-    *sms = cache[dev].load(std::memory_order_acquire);
-    if (*sms > 0) return cudaSuccess;
-    const cudaError_t e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) cache[dev].store(*sms, std::memory_order_release);
-    return e;
-}
-
-template <typename K, typename... Args>
-cudaError_t launch_pdl(K kernel, long long grid, int threads, size_t smem, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace
+
+template <typename T>
+static cudaError_t quant_rows_go(const T* x, long long ldx, long long M, long long K, uint8_t* q, float* sa,
+                                 cudaStream_t st) {
+    const long long nkb = (K + BLK - 1) / BLK, ctas = (M * ((nkb + RUN - 1) / RUN) + 7) / 8;
+    const long long grid = ctas < 16384 ? ctas : 16384;
+    const bool vec = K % 4 == 0 && ldx % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T)) == 0 &&
+                     reinterpret_cast<uintptr_t>(q) % 4 == 0;
+    return vec ? launch_pdl(quant_rows<T, true>, grid, 256, 0, st, x, ldx, M, (int)K, q, sa)
+               : launch_pdl(quant_rows<T, false>, grid, 256, 0, st, x, ldx, M, (int)K, q, sa);
+}
 
 cudaError_t launch_quant_rows(const void* x, int dtype, long long ldx, long long M, long long K, uint8_t* q, float* sa,
                               cudaStream_t st) {
-    const long long warps = M * ((K + BLK - 1) / BLK), grid = (warps + 7) / 8 < 16384 ? (warps + 7) / 8 : 16384;
-    if (dtype == kBf16)
-        return launch_pdl(quant_rows<__nv_bfloat16>, grid, 256, 0, st, static_cast<const __nv_bfloat16*>(x), ldx, M, (int)K,
-                          q, sa);
-    return launch_pdl(quant_rows<float>, grid, 256, 0, st, static_cast<const float*>(x), ldx, M, (int)K, q, sa);
+    if (dtype == kBf16) return quant_rows_go(static_cast<const __nv_bfloat16*>(x), ldx, M, K, q, sa, st);
+    return quant_rows_go(static_cast<const float*>(x), ldx, M, K, q, sa, st);
 }
 
 cudaError_t launch_quant_blocks(const void* w, long long N, long long K, uint8_t* q, float* sb, cudaStream_t st) {
-    const long long blocks = (N + BLK - 1) / BLK * ((K + BLK - 1) / BLK);
-    return launch_pdl(quant_blocks, blocks < 65536 ? blocks : 65536, 256, 0, st, static_cast<const __nv_bfloat16*>(w), N,
-                      (int)K, q, sb);
+    const long long blocks = (N + BLK - 1) / BLK * ((K + BLK - 1) / BLK), grid = blocks < 65536 ? blocks : 65536;
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(w);
+    const bool vec = K % 4 == 0 && reinterpret_cast<uintptr_t>(w) % 8 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0;
+    return vec ? launch_pdl(quant_blocks<true>, grid, 256, 0, st, p, N, (int)K, q, sb)
+               : launch_pdl(quant_blocks<false>, grid, 256, 0, st, p, N, (int)K, q, sb);
 }
 
 template <int NT>
@@ -737,7 +780,7 @@ cudaError_t fp8_gemm_tn(const uint8_t* A, const float* sa, const uint8_t* B, con
         if (e != cudaSuccess) return e;
         g_attr[dev].store(1, std::memory_order_release);
     }
-    if ((e = device_sms(dev, &sms)) != cudaSuccess) return e;
+    if ((sms = num_sms()) <= 0) return cudaErrorInvalidDevice;
     if (M <= 16) return thin_go<16>(A, sa, B, sb, D, M, N, K, ldd, alpha, dev, sms, st);
     if (M <= 32) return thin_go<32>(A, sa, B, sb, D, M, N, K, ldd, alpha, dev, sms, st);
     if (M <= 64) return thin_go<64>(A, sa, B, sb, D, M, N, K, ldd, alpha, dev, sms, st);

@@ -25,8 +25,10 @@
 //
 // Forward calls of few rows (norm_fwd_few) instead spread a row over more threads, one vector
 // each, straight from global memory: the shortest path through a row.
+#include "vl_api.h"
 #include "vl_device.cuh"
 #include "vl_internal.h"
+#include "vl_launch.h"
 #include "vl_pair.cuh"
 #include "vl_rowio.cuh"
 #include "vloss.h"
@@ -245,42 +247,54 @@ struct Safe {
 
 // ---------------------------------------------------------------- forward
 
-// Few rows: a row a CTA, one vector of V elements a thread.
-template <typename T, int V>
+// Few rows: a row a CTA, C vectors of V elements a thread.
+template <typename T, int V, int C>
 __global__ void __launch_bounds__(FEW) norm_fwd_few(const __grid_constant__ NormParams P) {
     __shared__ float2 red[2][FEW / 32];
     const int t = threadIdx.x, TH = blockDim.x, nv = P.hs / V;
     const long long r = blockIdx.x;
-    float ga[V], be[V], x[V], s = 0.f;
+    const bool wg = wide_affine(P.gamma, V), wb = wide_affine(P.beta, V);
+    float ga[C][V], be[C][V], x[C][V], s = 0.f;
     pdl_launch_dependents();
     pdl_wait_primary();
-    Vec<T, V> raw;
-    raw.zero();
-    if (t < nv) {
-        raw.load(static_cast<const T*>(P.x) + r * P.ldx + t * V);
-        load_affine<V>(P.gamma, t * V, wide_affine(P.gamma, V), 1.f, ga);
-        load_affine<V>(P.beta, t * V, wide_affine(P.beta, V), 0.f, be);
+    Vec<T, V> raw[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int q = t + c * TH;
+        raw[c].zero();
+        if (q < nv) {
+            raw[c].load(static_cast<const T*>(P.x) + r * P.ldx + q * V);
+            load_affine<V>(P.gamma, q * V, wg, 1.f, ga[c]);
+            load_affine<V>(P.beta, q * V, wb, 0.f, be[c]);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) s += raw.get(i);
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < V; ++i) s += raw[c].get(i);
     const float inv = 1.f / (float)P.hs;
     const float mu = group_sum(s, red[0], TH, 1) * inv;
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        x[i] = t < nv ? raw.get(i) - mu : 0.f;
-        s = fmaf(x[i], x[i], s);
-    }
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[c][i] = t + c * TH < nv ? raw[c].get(i) - mu : 0.f;
+            s = fmaf(x[c][i], x[c][i], s);
+        }
     const float var = group_sum(s, red[1], TH, 1) * inv;
     const float rstd = __frsqrt_rn(var + P.eps);
     if (t == 0) {
         if (P.mu_out) P.mu_out[r] = mu;
         if (P.rstd_out) P.rstd_out[r] = rstd;
     }
-    if (t < nv) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = fmaf(x[i] * rstd, ga[i], be[i]);
-        store_vec<T, V>(static_cast<T*>(P.y) + r * P.ldy + t * V, x);
+    for (int c = 0; c < C; ++c) {
+        const int q = t + c * TH;
+        if (q >= nv) break;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[c][i] = fmaf(x[c][i] * rstd, ga[c][i], be[c][i]);
+        store_vec<T, V>(static_cast<T*>(P.y) + r * P.ldy + q * V, x[c]);
     }
 }
 
@@ -614,39 +628,16 @@ __global__ void __launch_bounds__(256) norm_join(const __grid_constant__ NormPar
 
 constexpr int kMaxParts = 256;           // CTAs of the backward pass, at most
 
-int num_sms_dev() {
-    static std::atomic<int> cache[64];
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    sms = cache[dev].load(std::memory_order_acquire);
-    if (sms > 0) return sms;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    cache[dev].store(sms, std::memory_order_release);
-    return sms;
-}
-
-template <typename K, typename... Args>
-cudaError_t launch_pdl(K kernel, long long grid, dim3 threads, size_t smem, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = threads;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // Elements of a vector: bytes of x `vb` (16, 2 elements or 1) that every row start of every
 // operand allows.
 bool aligned(const void* p, long long ld, int es, int bytes) {
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * es % bytes == 0;
 }
 
-// Threads a row and rows a CTA of `threads` threads: 16 elements a thread where that fits.
+// Threads a row and rows a CTA of `threads` threads: 16 elements a thread in rows of up to `small`, else
+// 32.  Forward, small = 512: 16384 x 512 bf16 12.3 us with 16 and 14.1 with 32, 16384 x 4096 70 and
+// 56 (fewer threads meet at a row's sums).  Backward, 8192, all that 512 threads hold with 16 (the
+// column sums fill the registers with 32): 2048 x 4096 bf16 23 us with 16 and 35 with 32.
 struct Shape {
     int E, TH, groups;
 };
@@ -696,7 +687,7 @@ cudaError_t fwd_go(const NormParams& P, const Shape& s, cudaStream_t st) {
     static std::atomic<int> had[64];
     const cudaError_t e = opt_in(norm_fwd<T, V, E>, smem, had);
     if (e != cudaSuccess) return e;
-    const long long want = (P.rows + s.groups - 1) / s.groups, sms = num_sms_dev();
+    const long long want = (P.rows + s.groups - 1) / s.groups, sms = num_sms();
     return launch_pdl(norm_fwd<T, V, E>, want < sms ? want : sms, dim3(s.TH, s.groups), smem, st, P, depth,
                       safe_rows(P.x, P.ldx, sizeof(T), P.rows, P.hs));
 }
@@ -714,8 +705,16 @@ cudaError_t fwd(const NormParams& P, cudaStream_t st) {
         return P.hs % n == 0 && aligned(P.x, P.ldx, es, n * es) && aligned(P.y, P.ldy, es, n * es);
     };
     if (ok(N)) {
-        if (P.rows <= num_sms_dev() && P.hs <= FEW * N)
-            return launch_pdl(norm_fwd_few<T, N>, P.rows, dim3((P.hs / N + 31) / 32 * 32), 0, st, P);
+        // Few rows: a row a CTA (8 x 4096 bf16 2.1 us a call in a graph against 5.2 by the ring, 608 x
+        // 1024 2.1 and 4.9, 608 x 4096 5.6 and 6.8, fp32 7.6 and 8.1).
+        const int nv = P.hs / N;
+        if (P.rows <= 4 * num_sms() && nv <= 4 * FEW) {
+            const int C = nv <= FEW ? 1 : nv <= 2 * FEW ? 2 : 4;
+            const dim3 threads(((nv + C - 1) / C + 31) / 32 * 32);
+            if (C == 1) return launch_pdl(norm_fwd_few<T, N, 1>, P.rows, threads, 0, st, P);
+            if (C == 2) return launch_pdl(norm_fwd_few<T, N, 2>, P.rows, threads, 0, st, P);
+            return launch_pdl(norm_fwd_few<T, N, 4>, P.rows, threads, 0, st, P);
+        }
         return fwd_e<T, N>(P, st);
     }
     if (ok(2)) return fwd_e<T, 2>(P, st);
@@ -726,7 +725,7 @@ template <typename T, typename D, int V, int E>
 cudaError_t bwd_go(const NormParams& P, const Shape& s, cudaStream_t st) {
     const bool sums = P.dgamma || P.dbeta;
     long long grid = (P.rows + s.groups - 1) / s.groups;
-    const int sms = num_sms_dev(), most = sms < kMaxParts ? sms : kMaxParts;
+    const int sms = num_sms(), most = sms < kMaxParts ? sms : kMaxParts;
     if (grid > most) grid = most;
     const int stage = stage_bytes<T>(P.hs) + stage_bytes<D>(P.hs), depth = depth_of(s.groups, stage, RING_B);
     const size_t ring = (size_t)s.groups * depth * stage, meet = 8 * (size_t)P.hs, smem = ring > meet ? ring : meet;

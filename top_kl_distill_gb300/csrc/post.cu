@@ -29,6 +29,7 @@
 // not read, their gradient rows are zeroed.
 #include "vl_device.cuh"
 #include "vl_internal.h"
+#include "vl_launch.h"
 #include "vl_pair.cuh"
 #include "vl_rowio.cuh"
 #include "vloss.h"
@@ -403,7 +404,7 @@ __device__ __forceinline__ long long window_row(const PostParams& P, const Windo
 
 template <int MODE>
 __device__ Window deal(const PostParams& P, RSmem& S, long long w0, long long cid, long long ncl) {
-        if (P.ntok <= ncl) {                 // one row a cluster: taken as it is, its weight read with its data
+    if (P.ntok <= ncl) {                 // one row a cluster: taken as it is, its weight read with its data
         if (threadIdx.x == 0) S.list[0] = (int)cid;
         __syncthreads();
         return Window{0, 1, 1};
@@ -964,20 +965,6 @@ __global__ void __launch_bounds__(1024) total_kernel(const float* loss, long lon
     if (threadIdx.x == 0) *total = v.hi + v.lo;
 }
 
-template <typename K, typename... Args>
-cudaError_t launch_pdl(K kernel, long long grid, int threads, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 constexpr int kMaxDev = 64;
 
 int device() {
@@ -1058,9 +1045,9 @@ template <typename T, int MODE>
 cudaError_t launch_rows_t(const PostParams& P, cudaStream_t st) {
     constexpr int N = Pack<T>::N;
     const long long grid = P.ntok < (1 << 20) ? P.ntok : (1 << 20);
-    if (P.V <= 2048) return launch_pdl(rows_direct<T, MODE, 128, 16 / N>, grid, 128, st, P);
-    if (P.V <= 8192) return launch_pdl(rows_direct<T, MODE, 256, 32 / N>, grid, 256, st, P);
-    if (MODE == kPolicy && P.V > VL_POLICY_ONEPASS_COLS) return launch_pdl(rows_twice<T>, grid, NT, st, P);
+    if (P.V <= 2048) return launch_pdl(rows_direct<T, MODE, 128, 16 / N>, grid, 128, 0, st, P);
+    if (P.V <= 8192) return launch_pdl(rows_direct<T, MODE, 256, 32 / N>, grid, 256, 0, st, P);
+    if (MODE == kPolicy && P.V > VL_POLICY_ONEPASS_COLS) return launch_pdl(rows_twice<T>, grid, NT, 0, st, P);
     return launch_ring<T, MODE>(P, st);
 }
 
@@ -1074,14 +1061,14 @@ cudaError_t launch_post(const PostParams& P, cudaStream_t st) {
 cudaError_t launch_policy(const PostParams& P, float* total, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     if (P.ntok > 0) e = launch_post<kPolicy>(P, st);
-    if (e == cudaSuccess && total) e = launch_pdl(total_kernel, 1, 1024, st, (const float*)P.loss, P.ntok, total);
+    if (e == cudaSuccess && total) e = launch_pdl(total_kernel, 1, 1024, 0, st, (const float*)P.loss, P.ntok, total);
     return e;
 }
 
 cudaError_t launch_preference(const PostParams& P, const PairParams& Q, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     if (P.ntok > 0) e = launch_post<kLogp>(P, st);
-    if (e == cudaSuccess) e = launch_pdl(pair_kernel, kPairCtas, 1024, st, Q);
+    if (e == cudaSuccess) e = launch_pdl(pair_kernel, kPairCtas, 1024, 0, st, Q);
     if (e == cudaSuccess && P.ntok > 0 && P.g) e = launch_post<kGrad>(P, st);
     return e;
 }

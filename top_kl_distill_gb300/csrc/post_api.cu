@@ -10,7 +10,7 @@ using namespace vl;
 
 namespace {
 
-vl_status check_range(const void* p, const char* what, const char* fn) {
+vl_status check_ptr(const void* p, const char* what, const char* fn) {
     if (p == nullptr) return fail(VL_EINVAL, "%s: %s is NULL", fn, what);
     return VL_OK;
 }
@@ -54,9 +54,9 @@ vl_status policy_impl(const char* fn, const void* logits, int dtype, int64_t ld,
     if (!(clip_lo >= 0.f && clip_lo <= 1.f)) return fail(VL_EINVAL, "%s: clip_lo must be in [0, 1]", fn);
     if (!(clip_hi >= 0.f)) return fail(VL_EINVAL, "%s: clip_hi must be >= 0", fn);
     if (ntok > 0) {
-        if ((s = check_range(actions, "actions", fn)) || (s = check_range(old_logp, "old_logp", fn)) ||
-            (s = check_range(adv, "adv", fn)) || (s = check_range(weight, "weight", fn)) ||
-            (s = check_range(loss, "loss", fn)))
+        if ((s = check_ptr(actions, "actions", fn)) || (s = check_ptr(old_logp, "old_logp", fn)) ||
+            (s = check_ptr(adv, "adv", fn)) || (s = check_ptr(weight, "weight", fn)) ||
+            (s = check_ptr(loss, "loss", fn)))
             return s;
     } else if (total == nullptr) {
         return VL_OK;
@@ -100,10 +100,10 @@ vl_status preference_impl(const char* fn, const void* logits, int dtype, int64_t
         return fail(VL_EINVAL, "%s: unknown kind %d", fn, kind);
     if (!(beta > 0.f) || std::isinf(beta)) return fail(VL_EINVAL, "%s: beta must be positive", fn);
     if (!(smooth >= 0.f && smooth < 1.f)) return fail(VL_EINVAL, "%s: smooth must be in [0, 1)", fn);
-    if (ntok > 0 && ((s = check_range(labels, "labels", fn)) || (s = check_range(weight, "weight", fn)))) return s;
+    if (ntok > 0 && ((s = check_ptr(labels, "labels", fn)) || (s = check_ptr(weight, "weight", fn)))) return s;
     if (npairs > 0) {
-        if ((s = check_range(seq_start, "seq_start", fn)) || (s = check_range(loss, "loss", fn)) ||
-            (s = check_range(margin, "margin", fn)))
+        if ((s = check_ptr(seq_start, "seq_start", fn)) || (s = check_ptr(loss, "loss", fn)) ||
+            (s = check_ptr(margin, "margin", fn)))
             return s;
     } else if (mean == nullptr) {
         return VL_OK;
@@ -205,7 +205,7 @@ vl_status norm_bwd_impl(const char* fn, const void* dy, int dy_f32, int64_t lddy
                         int64_t lddx, float* dgamma, float* dbeta, void* ws, int64_t ws_bytes, void* stream) {
     vl_status s = check_norm(fn, x, "x", ldx, rows, hs);
     if (s || (s = check_norm(fn, dy, "dy", lddy, rows, hs)) || (s = check_norm(fn, dx, "dx", lddx, rows, hs))) return s;
-    if (rows > 0 && ((s = check_range(mu, "mu", fn)) || (s = check_range(rstd, "rstd", fn)))) return s;
+    if (rows > 0 && ((s = check_ptr(mu, "mu", fn)) || (s = check_ptr(rstd, "rstd", fn)))) return s;
     const int es = dtype == kBf16 ? 2 : 4, des = dy_f32 ? 4 : 2;
     if ((s = check_alias(fn, dx, "dx", lddx, es, x, "x", ldx, es, rows, hs)) ||
         (s = check_alias(fn, dx, "dx", lddx, es, dy, "dy", lddy, des, rows, hs)))

@@ -209,11 +209,6 @@ __device__ __forceinline__ void named_sync(uint32_t id, uint32_t n) {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(n) : "memory");
 }
 
-// Arrives at named barrier `id` over `n` threads without waiting for it.
-__device__ __forceinline__ void named_arrive(uint32_t id, uint32_t n) {
-    asm volatile("bar.arrive %0, %1;" :: "r"(id), "r"(n) : "memory");
-}
-
 // Named barrier that also returns how many participating threads passed pred = true.
 __device__ __forceinline__ uint32_t named_sync_popc(uint32_t id, uint32_t n, bool pred) {
     uint32_t r;

@@ -381,12 +381,23 @@ def vl_topk_rows_noalloc(logits, ld, ntok, V, k, loss_start, loss_end, ids, prob
 # ---------------------------------------------------------------- post-training
 
 
-def _ws(workspace, need, like):
-    """(address, bytes) of a workspace argument: 'auto' (the cached buffer of `like`'s device), a
-    tensor, (address, bytes), or None."""
+_stream_ws: dict = {}
+
+
+def _ws(workspace, need, like, stream):
+    """(address, bytes) of a workspace argument: 'auto' (a buffer kept for `like`'s device and the
+    call's stream, so that calls on two streams never share one), a tensor, (address, bytes), or None."""
     if workspace is None or need == 0:
         return None, 0
-    return _buf(workspace, need, like)
+    if not isinstance(workspace, str) or workspace != "auto":
+        return _buf(workspace, need, like)
+    torch = _torch or _load_torch()
+    dev = like.device.index if isinstance(like, torch.Tensor) else torch.cuda.current_device()
+    kept = _stream_ws.setdefault((dev, _stream(stream)), [])
+    if not kept or kept[-1].numel() < need:
+        # the smaller one stays alive: work that uses it may still be queued
+        kept.append(torch.empty(max(need, 2 * kept[-1].numel() if kept else 0), dtype=torch.uint8, device=f"cuda:{dev}"))
+    return kept[-1].data_ptr(), need
 
 
 def _policy(name, kind, logits, ld, ntok, V, actions, old_logp, ref_logp, adv, weight, clip_lo, clip_hi, kl_coef, scale,
@@ -417,7 +428,7 @@ def vl_preference_workspace_bytes(ntok, npairs) -> int:
 
 def _preference(name, dt, logits, ld, ntok, V, labels, weight, seq_start, npairs, ref_logp, beta, smooth, kind, scale, grad,
                 ldg, loss, margin, seq_logp, mean, err, workspace, stream):
-    ws, nb = _ws(workspace, vl_preference_workspace_bytes(ntok, npairs), logits)
+    ws, nb = _ws(workspace, vl_preference_workspace_bytes(ntok, npairs), logits, stream)
     _check(name, getattr(_lib or lib(), name)(
         _ptr(logits, dt, "logits"), ld, ntok, V, _ptr(labels, "u32", "labels"), _ptr(weight, "f32", "weight"),
         _ptr(seq_start, "i64", "seq_start"), npairs, _ptr(ref_logp, "f32", "ref_logp"), beta, smooth, kind, scale,
@@ -464,7 +475,7 @@ def vl_layernorm_bwd(dy, lddy, x, ldx, rows, hs, gamma, mu, rstd, dx, lddx, dgam
                      stream=None):
     """Layer norm backward, fp32.  workspace: 'auto' (a cached buffer), a tensor or (address, bytes)."""
     ws, nb = _ws(workspace if dgamma is not None or dbeta is not None else None, vl_layernorm_bwd_workspace_bytes(rows, hs),
-                 x)
+                 x, stream)
     _check("vl_layernorm_bwd", lib().vl_layernorm_bwd(
         _ptr(dy, "f32", "dy"), lddy, _ptr(x, "f32", "x"), ldx, rows, hs, _ptr(gamma, "f32", "gamma"), _ptr(mu, "f32", "mu"),
         _ptr(rstd, "f32", "rstd"), _ptr(dx, "f32", "dx"), lddx, _ptr(dgamma, "f32", "dgamma"), _ptr(dbeta, "f32", "dbeta"),
@@ -480,7 +491,7 @@ def vl_layernorm_bwd_bf16(dy, lddy, x, ldx, rows, hs, gamma, mu, rstd, dx, lddx,
             raise ValueError("dy_f32: needed when dy is a raw address")
         dy_f32 = dy is not None and str(dy.dtype) == "torch.float32"
     ws, nb = _ws(workspace if dgamma is not None or dbeta is not None else None, vl_layernorm_bwd_workspace_bytes(rows, hs),
-                 x)
+                 x, stream)
     _check("vl_layernorm_bwd_bf16", lib().vl_layernorm_bwd_bf16(
         _ptr(dy, "f32" if dy_f32 else "bf16", "dy"), 1 if dy_f32 else 0, lddy, _ptr(x, "bf16", "x"), ldx, rows, hs,
         _ptr(gamma, "f32", "gamma"), _ptr(mu, "f32", "mu"), _ptr(rstd, "f32", "rstd"), _ptr(dx, "bf16", "dx"), lddx,
