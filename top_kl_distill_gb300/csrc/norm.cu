@@ -6,16 +6,18 @@
 //
 // HBM bound: forward reads x and writes y, backward reads x and dy and writes dx, each once.
 //
-// One persistent CTA per SM; a row belongs to a group of T threads, 16 (or 32) elements a thread,
-// several groups a CTA.  A group's rows are fetched ahead of it by 1-D bulk copies (TMA) into its
+// One persistent CTA per SM; a row belongs to a group of T threads, 16, 32 or 64 elements a
+// thread, several groups a CTA.  A group's rows are fetched ahead of it by 1-D bulk copies (TMA) into its
 // ring in shared memory, a row a stage: one copy of each operand, issued by one thread.  (With a
 // cp.async per 16 bytes and thread instead, issuing the copies was half of the backward pass's
 // time.)  A row is read from its stage once, so the group's own sum, whose barrier every thread
 // passes after reading, is what frees the stage.  Backward threads keep their columns over all
 // rows: gamma stays in registers, and dgamma and dbeta build up there; forward keeps gamma and beta
-// in shared memory (from the caches, which the ring leaves 30 KB, they took half of a row's time).  Forward takes the mean, then
-// the squared deviations from it (no cancellation for rows far from zero), each one sum over the
-// group; backward one sum of two values.  The CTAs' column sums meet in a fixed order (the
+// in shared memory (from the caches, which the ring leaves 30 KB, they took half of a row's time).
+// Forward takes the mean, then the squared deviations from it (no cancellation for rows far from
+// zero), each one sum over the group (one meeting, with deviations from each warp's own mean, took
+// 49.6 us against 47.7 at 16384 x 4096 bf16); backward one sum of two values.  At that size forward
+// reaches 0.83 of the copy rate, backward (fp32 dy, 85 us) 0.93.  The CTAs' column sums meet in a fixed order (the
 // workspace, then one kernel over it): the same bits on every call.
 //
 // Alignment: a copy covers the 16-byte blocks that hold the row, so that it starts on a 16-byte
@@ -23,8 +25,8 @@
 // copies the row element by element.  Threads read 16 bytes of x (8 beside an fp32 dy of a bf16
 // row) at a time where addresses, strides and hs allow it, else 2 elements, else 1.
 //
-// Forward calls of few rows (norm_fwd_few) instead spread a row over more threads, one vector
-// each, straight from global memory: the shortest path through a row.
+// Forward calls of few rows (norm_fwd_few) instead spread a row over more threads, one to four
+// vectors each, straight from global memory: the shortest path through a row.
 #include "vl_api.h"
 #include "vl_device.cuh"
 #include "vl_internal.h"
@@ -40,6 +42,7 @@ namespace {
 
 constexpr int FEW = 512;                 // threads of a row at most, calls of few rows
 constexpr int FWD = 768, BWD = 512;      // threads of a CTA: up to 80 and 128 registers each
+constexpr int FWD64 = 512;               // forward with 64 elements a thread
 constexpr int RING_B = 192 * 1024;       // shared memory for rows in flight (forward: and gamma and beta)
 constexpr int MAXD = 8;                  // rows in flight a group
 constexpr int MAXG = FWD / 32;           // groups a CTA
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(FEW) norm_fwd_few(const __grid_constant__ Norm
 }
 
 template <typename T, int V, int E>
-__global__ void __launch_bounds__(FWD, 1) norm_fwd(const __grid_constant__ NormParams P, int depth, Safe safe) {
+__global__ void __launch_bounds__(E == 64 ? FWD64 : FWD, 1) norm_fwd(const __grid_constant__ NormParams P, int depth, Safe safe) {
     constexpr int U = E / V, E2 = E / 2;
     extern __shared__ __align__(128) unsigned char dyn[];     // the groups' rings; gamma, beta
     __shared__ Bars B;
@@ -634,22 +637,23 @@ bool aligned(const void* p, long long ld, int es, int bytes) {
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * es % bytes == 0;
 }
 
-// Threads a row and rows a CTA of `threads` threads: 16 elements a thread in rows of up to `small`, else
-// 32.  Forward, small = 512: 16384 x 512 bf16 12.3 us with 16 and 14.1 with 32, 16384 x 4096 70 and
-// 56 (fewer threads meet at a row's sums).  Backward, 8192, all that 512 threads hold with 16 (the
-// column sums fill the registers with 32): 2048 x 4096 bf16 23 us with 16 and 35 with 32.
+// Threads a row (E elements each) and rows a CTA of `threads` threads.
 struct Shape {
     int E, TH, groups;
 };
 
-Shape shape_of(int hs, int threads, int small) {
+Shape shape_of(int hs, int threads, int E) {
     Shape s;
-    s.E = hs <= small ? 16 : 32;
-    s.TH = ((hs + s.E - 1) / s.E + 31) / 32 * 32;
+    s.E = E;
+    s.TH = ((hs + E - 1) / E + 31) / 32 * 32;
     s.groups = threads / s.TH;
     if (s.TH > 32 && s.groups > 15) s.groups = 15;      // named barriers 1 .. 15
     return s;
 }
+
+// Backward: 16 elements a thread in all rows that 512 threads hold so (with 32 the column sums fill
+// the registers): 2048 x 4096 bf16 23 us, with 32 35.
+Shape bwd_shape(int hs) { return shape_of(hs, BWD, hs <= 16 * BWD ? 16 : 32); }
 
 int depth_of(int groups, int stage, int ring) {
     const int d = ring / (groups * stage);
@@ -680,8 +684,9 @@ cudaError_t opt_in(F kernel, size_t smem, std::atomic<int> (&had)[64]) {
 }
 
 template <typename T, int V, int E>
-cudaError_t fwd_go(const NormParams& P, const Shape& s, cudaStream_t st) {
+cudaError_t fwd_go(const NormParams& P, Shape s, cudaStream_t st) {
     const int stage = stage_bytes<T>(P.hs), affine = (8 * P.hs + 15) / 16 * 16;
+    while (s.groups > 1 && s.groups * stage + affine > RING_B) --s.groups;
     const int depth = depth_of(s.groups, stage, RING_B - affine);
     const size_t smem = (size_t)s.groups * depth * stage + affine;
     static std::atomic<int> had[64];
@@ -694,8 +699,16 @@ cudaError_t fwd_go(const NormParams& P, const Shape& s, cudaStream_t st) {
 
 template <typename T, int V>
 cudaError_t fwd_e(const NormParams& P, cudaStream_t st) {
-    const Shape s = shape_of(P.hs, FWD, 512);
-    return s.E == 16 ? fwd_go<T, V, 16>(P, s, st) : fwd_go<T, V, 32>(P, s, st);
+    // Fewer threads a row meet less at its sums: 16384 x 512 bf16 12.3 us with 16 elements each and 14.1
+    // with 32, 16384 x 4096 70 and 50.  64 pay in bf16 rows of 2048 to 8192 that fill their warps:
+    // 16384 x 2048 26.4 us against 29.3 with 32, x 4096 47.8 and 50.3, 8192 x 8192 46.1 and 52.4 (4096 x
+    // 12288 43.1 and 42.2; fp32 the same within 2%).
+    if (P.hs <= 512) return fwd_go<T, V, 16>(P, shape_of(P.hs, FWD, 16), st);
+    if constexpr (sizeof(T) == 2 && V == 8) {
+        const Shape s = shape_of(P.hs, FWD64, 64);
+        if (P.hs >= 2048 && P.hs <= 8192 && 64 * s.TH - P.hs <= P.hs / 4) return fwd_go<T, V, 64>(P, s, st);
+    }
+    return fwd_go<T, V, 32>(P, shape_of(P.hs, FWD, 32), st);
 }
 
 template <typename T>
@@ -742,7 +755,7 @@ cudaError_t bwd_go(const NormParams& P, const Shape& s, cudaStream_t st) {
 
 template <typename T, typename D, int V>
 cudaError_t bwd_e(const NormParams& P, cudaStream_t st) {
-    const Shape s = shape_of(P.hs, BWD, 16 * BWD);
+    const Shape s = bwd_shape(P.hs);
     return s.E == 16 ? bwd_go<T, D, V, 16>(P, s, st) : bwd_go<T, D, V, 32>(P, s, st);
 }
 
@@ -762,7 +775,7 @@ cudaError_t bwd(const NormParams& P, cudaStream_t st) {
 }  // namespace
 
 long long norm_bwd_ws_bytes(long long rows, long long hs) {
-    const Shape s = shape_of((int)hs, BWD, 16 * BWD);
+    const Shape s = bwd_shape((int)hs);
     const long long want = (rows + s.groups - 1) / s.groups;
     return (want < kMaxParts ? want : kMaxParts) * 2 * hs * 4;
 }

@@ -20,7 +20,7 @@
 //                two tiles.  Longer rows, and rows too few for the SMs, are split over a cluster;
 //                every warp sends its partial (max, sum) to every rank with st.async.
 //   short rows   (rows_direct, up to 8192 columns) a CTA of 128 or 256 threads a row, loaded straight
-//                into registers; many CTAs an SM overlap each other's phases.  A short row in the
+//                into registers; several CTAs an SM overlap each other's phases.  A short row in the
 //                ring kernel would leave most of its threads idle and pay a barrier a row.
 //   beyond       (rows_twice) rows of more than VL_POLICY_ONEPASS_COLS columns are read twice.
 //
@@ -1045,6 +1045,8 @@ template <typename T, int MODE>
 cudaError_t launch_rows_t(const PostParams& P, cudaStream_t st) {
     constexpr int N = Pack<T>::N;
     const long long grid = P.ntok < (1 << 20) ? P.ntok : (1 << 20);
+    // Policy, 4096 x 2048 fp32: 19 us with 128 threads, 42 with 256.  4096 x 8192: 60 us so, 80 by the ring;
+    // beyond, with 512 threads, one CTA fits an SM: 4096 x 8200 88 us, by the ring 77.
     if (P.V <= 2048) return launch_pdl(rows_direct<T, MODE, 128, 16 / N>, grid, 128, 0, st, P);
     if (P.V <= 8192) return launch_pdl(rows_direct<T, MODE, 256, 32 / N>, grid, 256, 0, st, P);
     if (MODE == kPolicy && P.V > VL_POLICY_ONEPASS_COLS) return launch_pdl(rows_twice<T>, grid, NT, 0, st, P);
