@@ -118,6 +118,16 @@ def test_norm(rows, hs, dtype, dyt):
 
 
 @pytest.mark.parametrize("dtype,dyt", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("rows,hs,pad,off", [(700, 64, 0, 0), (1300, 512, 0, 0), (640, 768, 8, 0), (640, 1024, 0, 8), (777, 2048, 0, 0),
+                                             (615, 4096, 0, 0), (612, 5120, 16, 0), (611, 8192, 0, 0), (609, 8200, 0, 0),
+                                             (609, 16384, 0, 0), (612, 2050, 0, 1), (613, 1500, 1, 0)])
+def test_norm_of_many_rows(rows, hs, pad, off, dtype, dyt):
+    """More rows than one CTA each takes at once: the persistent kernels, at every number of elements a thread."""
+    x, dy, ga, be = _case(rows, hs, dtype, dyt, rows * hs)
+    check(run(x, dy, ga, be, dtype, dyt, pad=pad, off=off), x, dy, ga, be, dtype)
+
+
+@pytest.mark.parametrize("dtype,dyt", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
 @pytest.mark.parametrize("hs,pad,off", [(512, 0, 1), (512, 5, 0), (1000, 8, 8), (2051, 0, 3), (4096, 3, 2), (9001, 7, 1)])
 def test_norm_strides_and_alignment(hs, pad, off, dtype, dyt):
     x, dy, ga, be = _case(11, hs, dtype, dyt, hs)
