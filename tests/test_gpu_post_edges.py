@@ -1,0 +1,43 @@
+"""How exactly the preference loss keeps the sums over a sequence.
+
+A row of two columns whose other logit c is 200 or more has the log-probability -c exactly (the
+picked column's exponential is below the smallest float, so m = c, ln S = 0), so that sums over
+such rows are known to the last bit from the inputs alone.
+"""
+from fractions import Fraction
+
+import numpy as np
+import pytest
+
+from tests.test_gpu_post_loss import run_pref
+
+pytestmark = pytest.mark.gpu
+
+
+def _exact_rows(c):
+    """Logits of rows whose label 0 has log-probability -c."""
+    return np.stack([np.zeros_like(c), c], 1).astype(np.float32)
+
+
+def _sum(w, c):
+    return sum((-Fraction(float(a)) * Fraction(float(b)) for a, b in zip(w, c)), Fraction(0))
+
+
+@pytest.mark.parametrize("n", [40, 129, 700])
+def test_margin_of_long_sequences(n):
+    """Sums of some -200 n less references of the same size: the margin is that of the inputs to a
+    few roundings of itself (the products with beta and the last sum: 4 * 2^-24) and 2^-40 of the sums."""
+    g = np.random.default_rng(n)
+    pairs = 4
+    c = g.uniform(200, 260, 2 * pairs * n).astype(np.float32)
+    w = np.where(np.arange(c.size) % n < n // 8, 0, g.uniform(0.5, 1.5, c.size)).astype(np.float32)
+    start = np.arange(2 * pairs + 1) * n
+    pi = [_sum(w[a:b], c[a:b]) for a, b in zip(start, start[1:])]
+    ref = np.array([float(p) for p in pi]) + 3 * g.normal(size=2 * pairs)
+    ref = ref.astype(np.float32)
+    beta = np.float32(0.1)
+    got = run_pref(_exact_rows(c), np.zeros(c.size, np.uint32), w, start, pairs, ref, float(beta), 0.1, 0, 1.0, "f32")
+    for i in range(pairs):
+        want = Fraction(float(beta)) * ((pi[i] - Fraction(float(ref[i]))) - (pi[pairs + i] - Fraction(float(ref[pairs + i]))))
+        tol = Fraction(4 * 2.0 ** -24) * abs(want) + Fraction(float(beta) * 2.0 ** -40) * (abs(pi[i]) + abs(pi[pairs + i]))
+        assert abs(Fraction(float(got["margin"][i])) - want) <= tol, (i, float(want), got["margin"][i])
