@@ -386,18 +386,34 @@ _stream_ws: dict = {}
 
 def _ws(workspace, need, like, stream):
     """(address, bytes) of a workspace argument: 'auto' (a buffer kept for `like`'s device and the
-    call's stream, so that calls on two streams never share one), a tensor, (address, bytes), or None."""
+    call's stream, so that calls on two streams never share one), a tensor, (address, bytes), or None.
+
+    The buffer is allocated on the call's stream too: the allocator hands out a freed block while kernels that use
+    it are still queued, which is safe only on the stream they are queued on.  A captured call gets none:
+    its graph may be replayed on any stream, beside calls on the one it was captured on."""
     if workspace is None or need == 0:
         return None, 0
     if not isinstance(workspace, str) or workspace != "auto":
         return _buf(workspace, need, like)
     torch = _torch or _load_torch()
     dev = like.device.index if isinstance(like, torch.Tensor) else torch.cuda.current_device()
-    kept = _stream_ws.setdefault((dev, _stream(stream)), [])
-    if not kept or kept[-1].numel() < need:
-        # the smaller one stays alive: work that uses it may still be queued
-        kept.append(torch.empty(max(need, 2 * kept[-1].numel() if kept else 0), dtype=torch.uint8, device=f"cuda:{dev}"))
-    return kept[-1].data_ptr(), need
+    s = _stream(stream)
+    if s == _stream(None) and dev == torch.cuda.current_device():
+        return _kept_ws(torch, dev, s, need)
+    # (a null handle would make ExternalStream take a stream from torch's pool)
+    with torch.cuda.stream(torch.cuda.ExternalStream(s, device=dev) if s else torch.cuda.default_stream(dev)):
+        return _kept_ws(torch, dev, s, need)
+
+
+def _kept_ws(torch, dev, s, need):
+    """The buffer kept for stream s, which is torch's current one."""
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("workspace='auto' cannot be captured in a graph: pass a workspace that lives as long as the graph")
+    kept = _stream_ws.get((dev, s))
+    if kept is None or kept.numel() < need:
+        grown = max(need, 0 if kept is None else 2 * kept.numel())
+        kept = _stream_ws[dev, s] = torch.empty(grown, dtype=torch.uint8, device=f"cuda:{dev}")
+    return kept.data_ptr(), need
 
 
 def _policy(name, kind, logits, ld, ntok, V, actions, old_logp, ref_logp, adv, weight, clip_lo, clip_hi, kl_coef, scale,
@@ -439,7 +455,7 @@ def _preference(name, dt, logits, ld, ntok, V, labels, weight, seq_start, npairs
 def vl_preference_loss(logits, ld, ntok, V, labels, weight, seq_start, npairs, ref_logp, beta, smooth, kind, scale, grad,
                        ldg, loss, margin, seq_logp=None, mean=None, err=None, workspace="auto", stream=None):
     """The preference loss over pairs of sequences and the gradient of the logits.  workspace:
-    'auto' (a cached buffer), a tensor or (address, bytes)."""
+    'auto' (a buffer kept for the stream; not in a captured call), a tensor or (address, bytes)."""
     _preference("vl_preference_loss", "f32", logits, ld, ntok, V, labels, weight, seq_start, npairs, ref_logp, beta,
                 smooth, kind, scale, grad, ldg, loss, margin, seq_logp, mean, err, workspace, stream)
 
@@ -473,7 +489,8 @@ def vl_layernorm_bwd_workspace_bytes(rows, hs) -> int:
 
 def vl_layernorm_bwd(dy, lddy, x, ldx, rows, hs, gamma, mu, rstd, dx, lddx, dgamma=None, dbeta=None, workspace="auto",
                      stream=None):
-    """Layer norm backward, fp32.  workspace: 'auto' (a cached buffer), a tensor or (address, bytes)."""
+    """Layer norm backward, fp32.  workspace: 'auto' (a buffer kept for the stream; not in a captured
+    call), a tensor or (address, bytes)."""
     ws, nb = _ws(workspace if dgamma is not None or dbeta is not None else None, vl_layernorm_bwd_workspace_bytes(rows, hs),
                  x, stream)
     _check("vl_layernorm_bwd", lib().vl_layernorm_bwd(
