@@ -462,6 +462,7 @@ VL_API vl_status vl_layernorm_bwd_bf16(const void* dy, int dy_f32, int64_t lddy,
  * makes its block's values 0 or NaN with an infinite scale, so that the product is NaN.
  * vl_quant_fp8_rows (fp32 x) / _bf16: blocks of 1 x 128, x [M][ldx] -> q [M][K], sa as above.
  * vl_quant_fp8_blocks_bf16: blocks of 128 x 128, w [N][K] bf16 (contiguous) -> q [N][K], sb.
+ * K is at most 2^30 in all of them.
  */
 VL_API vl_status vl_quant_fp8_rows(const float* x, int64_t ldx, int64_t M, int64_t K, uint8_t* q, float* sa,
                          void* stream);

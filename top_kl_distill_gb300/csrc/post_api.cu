@@ -242,7 +242,8 @@ vl_status norm_bwd_impl(const char* fn, const void* dy, int dy_f32, int64_t lddy
 
 vl_status quant_check(const char* fn, const void* x, int64_t ldx, int64_t M, int64_t K, const void* q, const void* sc) {
     if (M < 0 || K < 0) return fail(VL_EINVAL, "%s: negative size", fn);
-    if (K > (1LL << 31) || M > (1LL << 31)) return fail(VL_EINVAL, "%s: sizes must be at most 2^31", fn);
+    // the kernels count a row's columns in 32-bit ints, a few blocks past its end
+    if (K > (1LL << 30) || M > (1LL << 31)) return fail(VL_EINVAL, "%s: at most 2^31 rows of at most 2^30 columns", fn);
     if (ldx < K) return fail(VL_EINVAL, "%s: ldx (%lld) < K (%lld)", fn, (long long)ldx, (long long)K);
     if (M > 0 && ldx > 0 && M > (1LL << 62) / 4 / ldx) return fail(VL_EINVAL, "%s: M * ldx is out of range", fn);
     if (M > 0 && K > 0 && (!x || !q || !sc)) return fail(VL_EINVAL, "%s: NULL pointer", fn);
