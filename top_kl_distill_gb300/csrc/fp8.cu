@@ -117,8 +117,7 @@ __device__ __forceinline__ void st4(uint8_t* q, float4 v, float s, float inv, in
 constexpr int RUN = 4;
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) quant_rows(const T* __restrict__ x, long long ldx, long long M, int K,
-                                                  uint8_t* __restrict__ q, float* __restrict__ sa) {
+__global__ void __launch_bounds__(256) quant_rows(const T* x, long long ldx, long long M, int K, uint8_t* q, float* sa) {
     pdl_launch_dependents();
     pdl_wait_primary();
     const int nkb = (K + BLK - 1) / BLK, lane = threadIdx.x & 31;
@@ -148,8 +147,7 @@ __global__ void __launch_bounds__(256) quant_rows(const T* __restrict__ x, long 
 
 // One CTA a block of 128 x 128, 16 rows of it a warp, in registers between the two uses.
 template <bool VEC>
-__global__ void __launch_bounds__(256) quant_blocks(const __nv_bfloat16* __restrict__ w, long long N, int K,
-                                                    uint8_t* __restrict__ q, float* __restrict__ sb) {
+__global__ void __launch_bounds__(256) quant_blocks(const __nv_bfloat16* w, long long N, int K, uint8_t* q, float* sb) {
     __shared__ float red[8];
     pdl_launch_dependents();
     pdl_wait_primary();
@@ -279,8 +277,8 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32], uint32_t (&q)[32]) 
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
-    fp8_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const float* __restrict__ sa,
-             const float* __restrict__ sb, float* __restrict__ D, long long ldd, int M, int N, int K, float alpha,
+    fp8_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const float* sa,
+             const float* sb, float* D, long long ldd, int M, int N, int K, float alpha,
              int m_fast) {
     extern __shared__ uint8_t gsm_raw[];
     GSmem& S = *reinterpret_cast<GSmem*>((reinterpret_cast<uintptr_t>(gsm_raw) + 1023) & ~uintptr_t(1023));
@@ -548,8 +546,8 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
 // W [N][K] with scales sw [ceil(N/128)][nk]; X [M][K] with scales sx [nk][M]; D [M][ldd].
 template <int NT>
 __global__ void __launch_bounds__(192, 2)
-    fp8_gemm_thin(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const float* __restrict__ sw,
-                  const float* __restrict__ sx, float* __restrict__ D, long long ldd, int M, int N, int K, float alpha) {
+    fp8_gemm_thin(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const float* sw,
+                  const float* sx, float* D, long long ldd, int M, int N, int K, float alpha) {
     using C = Thin<NT>;
     extern __shared__ uint8_t gsm_raw[];
     TSmem<NT>& S = *reinterpret_cast<TSmem<NT>*>((reinterpret_cast<uintptr_t>(gsm_raw) + 1023) & ~uintptr_t(1023));

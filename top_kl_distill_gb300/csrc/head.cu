@@ -113,7 +113,7 @@ int head_dx(const void* g, long long rows, long long V, const void* w, const voi
 
 // fp32 -> bf16, nearest even (the page's cvt_cols of the gradient); both buffers
 // 16-byte aligned, any n.
-__global__ void cvt_bf16_kernel(const float* __restrict__ in, uint16_t* __restrict__ out, long long n) {
+__global__ void cvt_bf16_kernel(const float* in, uint16_t* out, long long n) {
     pdl_launch_dependents();
     pdl_wait_primary();
     const long long n4 = n / 4;

@@ -162,7 +162,8 @@ __device__ __forceinline__ void from_pairs(const uint64_t (&p)[U * V / 2], int u
     }
 }
 
-// V floats of an affine vector at column j (nullptr: `none`); wide: 4 V bytes a load.
+// V floats of an affine vector at column j (nullptr: `none`); wide: 4 V bytes a load.  The kernel before this one in
+// the stream may have written them (an optimiser's step).
 template <int V>
 __device__ __forceinline__ void load_affine(const float* p, int j, bool wide, float none, float (&f)[V]) {
     if (!p) {
@@ -172,14 +173,14 @@ __device__ __forceinline__ void load_affine(const float* p, int j, bool wide, fl
     }
     if constexpr (V == 8) {
         if (wide) {
-            asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                          : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
-                         : "l"(p + j));
+                         : "l"(p + j) : "memory");
             return;
         }
     } else if constexpr (V == 4) {
         if (wide) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p + j));
+            const float4 v = *reinterpret_cast<const float4*>(p + j);
             f[0] = v.x;
             f[1] = v.y;
             f[2] = v.z;
@@ -188,7 +189,7 @@ __device__ __forceinline__ void load_affine(const float* p, int j, bool wide, fl
         }
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = __ldg(p + j + i);
+    for (int i = 0; i < V; ++i) f[i] = p[j + i];
 }
 __device__ __forceinline__ bool wide_affine(const float* p, int V) {
     return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(4 * V - 1)) == 0;

@@ -740,7 +740,7 @@ __device__ void consumer(const float* x, long long ld, long long V, int k, const
 }
 
 __global__ void __maxnreg__(128)
-topk_kernel(const float* __restrict__ x, long long ld, long long V, int k, long long ls, long long le,
+topk_kernel(const float* x, long long ld, long long V, int k, long long ls, long long le,
             const int* list, const int* nlist, uint32_t* __restrict__ ids, float* __restrict__ probs, int* err) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     TSmem& S = *reinterpret_cast<TSmem*>(smem_raw);

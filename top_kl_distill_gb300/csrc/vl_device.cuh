@@ -220,7 +220,10 @@ __device__ __forceinline__ uint32_t named_sync_popc(uint32_t id, uint32_t n, boo
 }
 
 // Programmatic dependent launch: let the next kernel on the stream start its
-// prologue; it still waits for this grid's memory before reading it.
+// prologue; it still waits for this grid's memory before reading it.  What such a kernel
+// reads may still be written when it starts, so it is not read-only "for the kernel's
+// lifetime": no __ldg, ld.global.nc or const __restrict__ pointers (the compiler reads through
+// those by the same path, and may move such a read above the wait).
 __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -185,8 +185,7 @@ __device__ __forceinline__ void ff_add(float& hi, float& lo, float h2, float l2)
 // fixed order, so the result does not depend on the launch and needs no FP64 unit.
 // Launched as a programmatic dependent of the loss kernel: its launch overlaps that
 // kernel, griddepcontrol.wait holds it until the losses are in memory.
-__global__ void __launch_bounds__(1024) mean_kernel(const float* __restrict__ loss, long long ls, long long le,
-                                                    float* __restrict__ mean) {
+__global__ void __launch_bounds__(1024) mean_kernel(const float* loss, long long ls, long long le, float* mean) {
     pdl_launch_dependents();                 // the next kernel may start its set-up
     pdl_wait_primary();
     __shared__ float2 red[32];
