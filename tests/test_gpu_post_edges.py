@@ -23,6 +23,21 @@ def _sum(w, c):
     return sum((-Fraction(float(a)) * Fraction(float(b)) for a, b in zip(w, c)), Fraction(0))
 
 
+def test_sequence_sums_keep_48_bits():
+    """Terms of some 1000 that cancel to less than 0.1: each term's rounding to fp32 would be
+    far larger than what is allowed here, 2^-24 of the sum and 2^-40 of its terms' sizes."""
+    g = np.random.default_rng(5)
+    n = 600
+    c = g.uniform(200, 2000, n).astype(np.float32)
+    w = g.uniform(0.3, 1.7, n).astype(np.float32)
+    c[1::2], w[1::2] = c[::2], -w[::2] * np.float32(1 - 1e-4)
+    half = n // 2
+    got = run_pref(_exact_rows(c), np.zeros(n, np.uint32), w, [0, half, n], 1, None, 0.125, 0.0, 1, 1.0, "f32")
+    for s, sl in enumerate((slice(0, half), slice(half, n))):
+        want, size = _sum(w[sl], c[sl]), float(np.abs(w[sl].astype(np.float64) * c[sl]).sum())
+        assert abs(Fraction(float(got["seq"][s])) - want) <= Fraction(2.0 ** -24) * abs(want) + Fraction(2.0 ** -40 * size)
+
+
 @pytest.mark.parametrize("n", [40, 129, 700])
 def test_margin_of_long_sequences(n):
     """Sums of some -200 n less references of the same size: the margin is that of the inputs to a

@@ -829,24 +829,26 @@ __global__ void __launch_bounds__(RT, 1) rows_ring(const __grid_constant__ PostP
 // ---------------------------------------------------------------- pairs
 
 // Unevaluated pairs of floats (about 48 bits): the sums over a sequence and over the rows. The
-// card's 64-bit rate is far below its 32-bit one (the pair kernel took 11 us with doubles).
+// card's 64-bit rate is far below its 32-bit one (the pair kernel took 11 us with doubles).  Each
+// operation rounds by itself: a product fused into one of two_sum's additions would leave its low
+// part counted twice.
 struct FF {
     float hi, lo;
 };
 __device__ __forceinline__ FF two_sum(float a, float b) {
-    const float s = a + b, bb = s - a;
-    return FF{s, (a - (s - bb)) + (b - bb)};
+    const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+    return FF{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
 }
 __device__ __forceinline__ FF ff_add(FF a, FF b) {
     const FF s = two_sum(a.hi, b.hi);
     // an infinite or NaN sum has no error term (inf - inf would make one)
-    const float e = isfinite(s.hi) ? s.lo + (a.lo + b.lo) : 0.f;
-    const float h = s.hi + e;
-    return FF{h, isfinite(h) ? e - (h - s.hi) : 0.f};
+    const float e = isfinite(s.hi) ? __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)) : 0.f;
+    const float h = __fadd_rn(s.hi, e);
+    return FF{h, isfinite(h) ? __fsub_rn(e, __fsub_rn(h, s.hi)) : 0.f};
 }
 __device__ __forceinline__ FF ff_mul(float a, float b) {
-    const float p = a * b;
-    return FF{p, isfinite(p) ? fmaf(a, b, -p) : 0.f};
+    const float p = __fmul_rn(a, b);
+    return FF{p, isfinite(p) ? __fmaf_rn(a, b, -p) : 0.f};
 }
 
 __device__ __forceinline__ FF warp_sum_ff(FF v) {

@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(1024) mean_kernel(const float* loss, long long
             // (hi + lo) / n: the quotient of the pair, one correction step
             const float n = (float)(le - ls);
             float q = hi / n, pe;
-            const float p = q * n;
+            const float p = __fmul_rn(q, n);         // (fused into hi - p, pe would count twice)
             pe = fmaf(q, n, -p);                     // q * n = p + pe exactly
             q += ((hi - p) - pe + lo) / n;
             *mean = le > ls ? q : 0.0f;
