@@ -403,6 +403,9 @@ VL_API vl_status vl_policy_loss_bf16(const uint16_t* logits, int64_t ld, int64_t
  *   aligned, no initial contents needed; calls that share one must not overlap on the GPU.
  * A pair with a label >= V (in a row of weight != 0) has loss, margin and pi_s NaN and zero
  * gradient rows; each such label is counted in *err.
+ * A label of probability 0 (logit -inf) makes its pi_s -inf.  In the rejected sequence: margin +inf and, without
+ * smoothing, loss 0 and no gradient; in the chosen one: loss +inf and the slope's limit in the gradient (the
+ * squared loss has no limit: its gradient is not finite); in both: NaN.
  */
 typedef enum vl_pref_kind { VL_PREF_SIGMOID = 0, VL_PREF_IPO = 1, VL_PREF_HINGE = 2 } vl_pref_kind;
 VL_API int64_t vl_preference_workspace_bytes(int64_t ntok, int64_t npairs);

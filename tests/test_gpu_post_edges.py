@@ -1,4 +1,4 @@
-"""How exactly the preference loss keeps the sums over a sequence.
+"""How exactly the preference loss keeps the sums over a sequence, and values at the ends of their ranges.
 
 A row of two columns whose other logit c is 200 or more has the log-probability -c exactly (the
 picked column's exponential is below the smallest float, so m = c, ln S = 0), so that sums over
@@ -12,6 +12,7 @@ import pytest
 from tests.test_gpu_post_loss import run_pref
 
 pytestmark = pytest.mark.gpu
+INF = float("inf")
 
 
 def _exact_rows(c):
@@ -56,3 +57,31 @@ def test_margin_of_long_sequences(n):
         want = Fraction(float(beta)) * ((pi[i] - Fraction(float(ref[i]))) - (pi[pairs + i] - Fraction(float(ref[pairs + i]))))
         tol = Fraction(4 * 2.0 ** -24) * abs(want) + Fraction(float(beta) * 2.0 ** -40) * (abs(pi[i]) + abs(pi[pairs + i]))
         assert abs(Fraction(float(got["margin"][i])) - want) <= tol, (i, float(want), got["margin"][i])
+
+
+@pytest.mark.parametrize("V", [40, 3000, 9000])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_preference_of_impossible_labels(V, dtype):
+    """A label of probability 0 (logit -inf) in the rejected sequence: the pair is won beyond doubt,
+    loss 0, nothing to learn; in the chosen one the loss is infinite and the gradient is beta's."""
+    g = np.random.default_rng(V)
+    x = (g.integers(-8, 9, (8, V)) * 0.5).astype(np.float32)
+    lab = g.integers(0, V, 8).astype(np.uint32)
+    start = [0, 2, 4, 6, 8]                                  # pairs (0, 2) and (1, 3) of sequences of two rows
+    x[[2, 3, 6, 7], lab[[2, 3, 6, 7]]] = 0.0                 # pair 1 is close
+    x[5, lab[5]] = -np.inf                                   # sequence 2: rejected in pair 0
+    w = np.ones(8, np.float32)
+    for kind, won in ((0, 0.0), (2, 0.0)):
+        got = run_pref(x, lab, w, start, 2, None, 0.5, 0.0, kind, 1.0, dtype)
+        assert got["margin"][0] == INF and got["seq"][2] == -INF and got["loss"][0] == won, (kind, got["loss"])
+        assert np.isfinite(got["loss"][1]) and got["mean"] == pytest.approx(got["loss"][1] / 2, rel=1e-6)
+        assert not got["grad"][[0, 1, 4, 5]].any() and got["grad"][[2, 3, 6, 7]].any()
+    got = run_pref(x, lab, w, start, 2, None, 0.5, 0.1, 0, 1.0, dtype)        # smoothed: the doubt costs without end
+    assert got["loss"][0] == INF
+    x[5, lab[5]], x[0, lab[0]] = 1.0, -np.inf                # now the chosen one
+    got = run_pref(x, lab, w, start, 2, None, 0.5, 0.0, 0, 1.0, dtype)
+    assert got["margin"][0] == -INF and got["loss"][0] == INF and np.isfinite(got["grad"]).all()
+    assert got["grad"][0, lab[0]] == -0.5                    # beta ([j == a] - 0), a step up
+    # impossible on both sides: no answer
+    x[5, lab[5]] = -np.inf
+    assert np.isnan(run_pref(x, lab, w, start, 2, None, 0.5, 0.0, 0, 1.0, dtype)["loss"][0])

@@ -918,7 +918,8 @@ __global__ void __cluster_dims__(kPairCtas, 1, 1) __launch_bounds__(1024) pair_k
         const float h = Q.beta * gap.hi + Q.beta * gap.lo;
         float loss, d;                              // d loss / d gap
         if (Q.kind == VL_PREF_SIGMOID) {
-            loss = (1.f - Q.smooth) * softplus(-h) + Q.smooth * softplus(h);
+            loss = (1.f - Q.smooth) * softplus(-h);
+            if (Q.smooth != 0.f) loss += Q.smooth * softplus(h);      // (0 times infinity where h is infinite)
             // sigmoid(h) - (1 - smooth), each tail from the side that does not cancel
             const float e = expf(-fabsf(h)), small = e / (1.f + e);
             d = Q.beta * (h >= 0.f ? Q.smooth - small : small - (1.f - Q.smooth));
