@@ -9,7 +9,7 @@ from fractions import Fraction
 import numpy as np
 import pytest
 
-from tests.test_gpu_post_loss import run_pref
+from tests.test_gpu_post_loss import run_policy, run_pref
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -85,3 +85,31 @@ def test_preference_of_impossible_labels(V, dtype):
     # impossible on both sides: no answer
     x[5, lab[5]] = -np.inf
     assert np.isnan(run_pref(x, lab, w, start, 2, None, 0.5, 0.0, 0, 1.0, dtype)["loss"][0])
+
+
+@pytest.mark.parametrize("V", [40, 3000, 9000])
+@pytest.mark.parametrize("hi", [0.28, INF])
+def test_policy_of_no_advantage(V, hi):
+    """An advantage of 0 costs nothing and teaches nothing, however far the ratio has gone (here past
+    the largest float: the sampler's log-probability was below -89, or it was -inf)."""
+    g = np.random.default_rng(V)
+    n = 6
+    x = (g.normal(size=(n, V)) * 2).astype(np.float32)
+    act = g.integers(0, V, n).astype(np.uint32)
+    old = np.array([-120.0, -np.inf, -8.0, -150.0, -1e30, -8.0], np.float32)
+    adv = np.array([0.0, -0.0, 0.0, 0.0, 0.0, 1.0], np.float32)
+    w = np.ones(n, np.float32)
+    got = run_policy(x, act, old, None, adv, w, 0.0, 1.0, "f32", hi=hi)
+    assert not got["loss"][:5].any() and not got["grad"][:5].any() and np.isfinite(got["total"]), got["loss"]
+    # beside a KL term that is all there is
+    ref = np.full(n, -9.0, np.float32)
+    a = run_policy(x, act, old, ref, adv, w, 0.5, 1.0, "f32", hi=hi)
+    b = run_policy(x, act, np.full(n, -8.0, np.float32), ref, np.where(adv == 0, 0, adv).astype(np.float32), w, 0.5, 1.0, "f32", hi=hi)
+    assert np.isfinite(a["loss"]).all() and np.array_equal(a["loss"], b["loss"]) and np.array_equal(a["grad"], b["grad"])
+    # with an advantage the vast ratio counts: clipped on the side that gains, without bound on the other
+    adv = np.array([1.0, 1.0, 1.0, -1.0, -2.0, 1.0], np.float32)
+    got = run_policy(x, act, old, None, adv, w, 0.0, 1.0, "f32", hi=0.28)
+    assert np.allclose(got["loss"][:2], -1.28, rtol=1e-6) and got["loss"][3] == INF and got["loss"][4] == INF
+    # NaN stays NaN
+    x[0, 1] = np.nan
+    assert np.isnan(run_policy(x, act, old, None, adv * 0, w, 0.0, 1.0, "f32", hi=hi)["loss"][0])

@@ -52,7 +52,8 @@ struct Outcome {
 
 // The losses of one token.  Comparisons are arranged so that a NaN stays a NaN.
 __device__ __forceinline__ Outcome policy_outcome(const PostParams& P, float w, float old, float ref, float A, float logp) {
-    const float ratio = expf(logp - old);
+    const float e0 = expf(logp - old);
+    const float ratio = A == 0.f && isinf(e0) ? 1.f : e0;      // no advantage: 0 however far the ratio went, not 0 inf
     const float f = ratio * A;
     const float h = (ratio < P.lo ? P.lo : ratio > P.hi ? P.hi : ratio) * A;
     const bool capped = f > h;
