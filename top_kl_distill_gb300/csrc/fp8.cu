@@ -91,7 +91,7 @@ __device__ __forceinline__ float reciprocal_of(float s) {
 }
 __device__ __forceinline__ float quotient(float x, float s, float inv) {
     const float p = x * inv;
-    return fmaf(fmaf(-p, s, x), inv, p);
+    return fmaf(fmaf(p, s, -x), -inv, p);       // signs so that a residual of 0 leaves -0 as it is
 }
 
 template <bool VEC>
