@@ -379,8 +379,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         float* const stage = S.out[warp - 4];
         const uint32_t tempty[2] = {map_to_rank(&S.tempty[0], 0), map_to_rank(&S.tempty[1], 0)};
         uint32_t g = 0;
-        bool stop = false;
-        for (int t = cid; t < tiles && !stop; t += ncl) {
+        bool lost = false;
+        for (int t = cid; t < tiles; t += ncl) {
             int m0, n0;
             tile_at(t, m0, n0);
             const int r0 = m0 + HALF * rank + 32 * q, c0 = n0 + 128 * half;
@@ -400,10 +400,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     na = sap[(long long)(kb + 1) * M];
                     nb = sbp[kb + 1];
                 }
-                if (!wait_parity<false>(&S.tfull[b], (g >> 1) & 1u, &S.abort, &g_watchdog)) {
-                    stop = true;
-                    break;
-                }
+                // A lane whose wait ran out goes on with the others: a tensor-memory load is the whole warp's.  (Agreeing
+                // on it at every block costs 1.5% at 2048 x 128256 x 4096.)
+                lost = lost || !wait_parity<false>(&S.tfull[b], (g >> 1) & 1u, &S.abort, &g_watchdog);
                 tc_fence_after();
                 const uint32_t ta0 = tmem + ((uint32_t)(32 * q) << 16) + b * (uint32_t)BN + 128u * half;
                 if (any) {
@@ -424,14 +423,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     tmem_ld32(ta0 + 96u, v[1]);
                     tmem_wait(v[0], v[1]);
                     tc_fence_before();                // the buffer has been read
-                    if (lane == 0) arrive_cluster(tempty[b]);
+                    if (lane == 0 && !lost) arrive_cluster(tempty[b]);
                     add(2);
                     add(3);
-                } else if (lane == 0) {
+                } else if (lane == 0 && !lost) {
                     arrive_cluster(tempty[b]);
                 }
             }
-            if (stop || !any) continue;
+            if (__any_sync(0xffffffffu, lost) || !any) continue;
             const uint64_t al = both(alpha);
             const int rows = min(32, M - r0);
 #pragma unroll
@@ -631,7 +630,7 @@ __global__ void __launch_bounds__(192, 2)
         constexpr int PER = XB * NT / 128;           // scales of a batch that a thread brings
         const int q = warp & 3, tid = threadIdx.x - 64;
         uint32_t g = 0, batch = 0;
-        bool stop = false;
+        bool lost = false;               // a wait ran out: the warp goes on through the barriers alone, which the others pass
         float na[PER], nb[PER];
         auto bring = [&](int t, int k0) {
 #pragma unroll
@@ -643,11 +642,11 @@ __global__ void __launch_bounds__(192, 2)
             }
         };
         bring(blockIdx.x, 0);
-        for (int t = blockIdx.x; t < tiles && !stop; t += gridDim.x) {
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
             uint64_t acc[NT / 2];
 #pragma unroll
             for (int j = 0; j < NT / 2; ++j) acc[j] = 0;
-            for (int k0 = 0; k0 < nk && !stop; k0 += XB, ++batch) {
+            for (int k0 = 0; k0 < nk; k0 += XB, ++batch) {
                 float* const sc = &S.scale[batch & 1u][0][0];
 #pragma unroll
                 for (int i = 0; i < PER; ++i) sc[tid + 128 * i] = na[i] * nb[i];
@@ -657,7 +656,7 @@ __global__ void __launch_bounds__(192, 2)
                 for (int kb = k0; kb < min(k0 + XB, nk); ++kb, ++g) {
                     const uint32_t b = g & 1u;
                     if (!wait_all(&S.tfull[b], (g >> 1) & 1u, &S.abort)) {
-                        stop = true;
+                        lost = true;
                         break;
                     }
                     tc_fence_after();
@@ -684,7 +683,7 @@ __global__ void __launch_bounds__(192, 2)
                 }
             }
             const int n = t * BLK + 32 * q + lane;
-            if (!stop && n < N) {
+            if (!lost && n < N) {
 #pragma unroll
                 for (int j = 0; j < NT / 2; ++j) {
                     float x, y;

@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(GT, 1) tc_gemm_kernel(const __grid_constant__ 
         uint32_t i = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
             const uint32_t b = i & 1u;
-            if (!wait_parity<false>(&S.tfull[b], (i >> 1) & 1u, &S.abort, &g_watchdog)) break;
+            // all lanes agree on whether it gave up: a tensor-memory load is the whole warp's
+            if (!__all_sync(0xffffffffu, wait_parity<false>(&S.tfull[b], (i >> 1) & 1u, &S.abort, &g_watchdog))) break;
             tc_fence_after();
             int m0, n0;
             tile_at(t, m0, n0);
