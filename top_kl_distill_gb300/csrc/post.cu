@@ -405,16 +405,18 @@ __device__ __forceinline__ long long window_row(const PostParams& P, const Windo
 
 template <int MODE>
 __device__ Window deal(const PostParams& P, RSmem& S, long long w0, long long cid, long long ncl) {
-    if (P.ntok <= ncl) {                 // one row a cluster: taken as it is, its weight read with its data
+    const float* wt = MODE == kGrad ? P.coef : P.weight;
+    Window W{w0, 0, 0};
+    if (P.ntok <= ncl) {                 // one row a cluster
         if (threadIdx.x == 0) S.list[0] = (int)cid;
         __syncthreads();
-        return Window{0, 1, 1};
+        W.n = 1;
+        W.live = wt[window_row<MODE>(P, W, (int)cid)] != 0.f;
+        return W;
     }
     const int n = (int)min(P.ntok - w0, ncl * kWindow);
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int per = (n + RT - 1) / RT * 32, lo = wp * per, hi = min(n, lo + per);
-    const float* wt = MODE == kGrad ? P.coef : P.weight;
-    Window W{w0, 0, 0};
     auto counts = [&](int k) { return k < hi && wt[window_row<MODE>(P, W, k)] != 0.f; };
     int mine = 0;
     uint64_t flags = 0;                  // this lane's rows lo + 32 q + lane, bit q (a window is cut to fit)
@@ -602,11 +604,6 @@ __device__ void ring_consumer(const PostParams& P, RSmem& S, int rank, int c, co
             // the row's statistics are known: each tile turned into gradient as it lands
             meta_ready();
             const float m = mt.xa, lnS = mt.old, f0 = mt.w;
-            if (f0 == 0.f) {                         // (one row a cluster) no weight after all
-                for (int t = 0; t < nt; ++t, ++g) release(await(g));
-                store_zeros();
-                continue;
-            }
             const uint64_t nm = pack2(-m, -m), nl = pack2(-lnS, -lnS), f2 = pack2(-f0, -f0);
             for (int t = 0; t < nt; ++t, ++g) {
                 const uint32_t slot = await(g);
@@ -723,7 +720,7 @@ __device__ void ring_consumer(const PostParams& P, RSmem& S, int rank, int c, co
         }
         if (cw == 0) {
             meta_ready();
-            const bool bad = !mt.live;               // a column past the row, or no weight after all
+            const bool bad = !mt.live;               // a column past the row
             MaxSum tot;
             if (c > 1) {
                 wait_parity<true>(&S.pbar[pb], ppar, &S.abort, &g_watchdog);
