@@ -343,8 +343,9 @@ VL_API vl_status vl_acc_add(float* a, const float* b, int64_t n, void* stream);
  *    or padding token) is not read at all (its logits may be anything, NaN included), has
  *    loss, log-probability and KL 0 and a zero gradient row.
  *  - `grad` [ntok][ldg] receives the gradient of the logits, in the logits' type; it may be
- *    `logits` itself (then ldg == ld: in place), must not overlap it otherwise, and may be
- *    NULL where no gradient is wanted.  Writes are 16 bytes wide when grad and logits rows
+ *    `logits` itself (then ldg == ld: in place), must not overlap it otherwise (rows of the same
+ *    stride may lie between its rows, as the halves of a wider buffer do), and may be NULL
+ *    where no gradient is wanted.  Writes are 16 bytes wide when grad and logits rows
  *    agree in their alignment modulo 16 bytes, else narrower (same results).
  *  - a logit of -inf is an ordinary value (probability 0).
  *  - scaling logits by a temperature belongs to the head's product (its alpha).
@@ -426,7 +427,7 @@ VL_API vl_status vl_preference_loss_bf16(const uint16_t* logits, int64_t ld, int
  *     y  = xh gamma + beta
  *   x [rows][ldx], y [rows][ldy] fp32, or bf16 in the _bf16 calls (sums in fp32, each output
  *   rounded once); gamma, beta [hs] fp32 (nullable: 1 and 0); mu, rstd [rows] fp32 (nullable).
- *   y may be x itself (ldy == ldx).  1 <= hs <= VL_NORM_MAX_HS; any alignment and strides.
+ *   y may be x itself (ldy == ldx), or lie between its rows.  1 <= hs <= VL_NORM_MAX_HS; any alignment and strides.
  * Backward, with t = dy gamma:
  *     dx = rstd (t - mean(t) - xh mean(t xh)),  dgamma = sum over rows of dy xh,  dbeta = sum of dy
  *   dy fp32 (in the _bf16 call: bf16, or fp32 when dy_f32 != 0, as the head's products hand

@@ -25,6 +25,19 @@ long long span(long long rows, long long ld, long long cols, int es) {
     return rows > 0 ? ((rows - 1) * ld + cols) * es : 0;
 }
 
+// Whether two matrices of the same number of rows and columns share bytes.  Rows of one stride may lie between
+// one another (the two halves of a wider buffer); of different strides, one matrix has to end before the other.
+bool overlap_rows(const void* a, long long lda, int aes, const void* b, long long ldb, int bes, long long rows,
+                  long long cols) {
+    if (!overlap(a, span(rows, lda, cols, aes), b, span(rows, ldb, cols, bes))) return false;
+    const long long pitch = lda * aes;
+    if (rows < 2 || pitch != ldb * bes) return true;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const long long ahead = (long long)((x < y ? y - x : x - y) % (uintptr_t)pitch);
+    const long long d = x < y || ahead == 0 ? ahead : pitch - ahead;       // from a row of a to the next start of one of b
+    return d < cols * aes || d + cols * bes > pitch;
+}
+
 // The logits and gradient of a post-training call.
 vl_status check_logits(const void* x, int64_t ld, int64_t ntok, int64_t V, const void* g, int64_t ldg, int es,
                        const char* fn) {
@@ -38,7 +51,7 @@ vl_status check_logits(const void* x, int64_t ld, int64_t ntok, int64_t V, const
         if (ntok > (1LL << 62) / 4 / ldg) return fail(VL_EINVAL, "%s: ntok * ldg is out of range", fn);
         if (g == x) {
             if (ldg != ld) return fail(VL_EINVAL, "%s: in place needs ldg == ld", fn);
-        } else if (overlap(x, span(ntok, ld, V, es), g, span(ntok, ldg, V, es))) {
+        } else if (overlap_rows(x, ld, es, g, ldg, es, ntok, V)) {
             return fail(VL_EINVAL, "%s: grad overlaps logits (it may be logits itself, or apart from it)", fn);
         }
     }
@@ -167,7 +180,7 @@ vl_status check_norm(const char* fn, const void* p, const char* what, int64_t ld
 vl_status check_alias(const char* fn, const void* out, const char* oname, int64_t ldo, int oes, const void* in,
                       const char* iname, int64_t ldi, int ies, int64_t rows, int64_t hs) {
     if (out == in && ldo == ldi && oes == ies) return VL_OK;
-    if (overlap(out, span(rows, ldo, hs, oes), in, span(rows, ldi, hs, ies)))
+    if (overlap_rows(out, ldo, oes, in, ldi, ies, rows, hs))
         return fail(VL_EINVAL, "%s: %s overlaps %s (it may be %s itself, with the same type and stride)", fn, oname, iname,
                     iname);
     return VL_OK;
