@@ -1,10 +1,10 @@
-"""The quantisers' zeros."""
+"""The quantisers' zeros, and few-row products of more tiles than CTAs.  Tolerances as in test_gpu_fp8.py."""
 import numpy as np
 import pytest
 
 from oracle import post_oracle as O
 from tests import gpu_harness as H
-from tests.test_gpu_fp8 import _bf, _data
+from tests.test_gpu_fp8 import _bf, _data, product
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +36,9 @@ def test_quantise_keeps_the_sign_of_zero(K, dtype):
         vl.vl_quant_fp8_blocks_bf16(t.to(torch.bfloat16), M, K, q, s)
         wq, ws = O.quant_blocks(x)
         assert np.array_equal(H.host(s), ws) and np.array_equal(H.host(q), wq)
+
+
+@pytest.mark.parametrize("M", [3, 20, 50])
+def test_product_of_few_rows_and_many_tiles(M):
+    """More 128-row tiles of the plane than two CTAs an SM take at once, and more than one batch of scales."""
+    product(M, 40001, 1040)
