@@ -25,13 +25,14 @@ def _blocks(n):
 
 
 class Head:
-    """A frozen head plane w [V][hs] (bf16; V and hs multiples of 16), quantised once: as it is for the logits, and
-    transposed for the way back."""
+    """A frozen head plane w [V][hs] (bf16; hs a multiple of 16), quantised once: as it is for the logits, and
+    transposed for the way back, with columns of zeros up to ld, the next multiple of 16 from V."""
 
     def __init__(self, w):
         self.V, self.hs = w.shape
+        self.ld = -(-self.V // 16) * 16
         self.plane = self._quantise(w)
-        self.back = self._quantise(w.t().contiguous())
+        self.back = self._quantise(torch.nn.functional.pad(w.t(), (0, self.ld - self.V)).contiguous())
 
     @staticmethod
     def _quantise(w):
@@ -46,7 +47,7 @@ class Step:
     """The buffers of a step over n rows, and the step itself."""
 
     def __init__(self, head, n):
-        V, hs = head.V, head.hs
+        ld, hs = head.ld, head.hs
         self.head, self.n = head, n
 
         def f32(*shape):
@@ -58,8 +59,9 @@ class Step:
         self.y = torch.empty(n, hs, dtype=torch.bfloat16, device="cuda")
         self.mu, self.rstd = f32(n), f32(n)
         self.yq, self.ys = u8(n, hs), f32(_blocks(hs), n)
-        self.logits = f32(n, V)                     # the gradient, after the loss
-        self.gq, self.gs = u8(n, V), f32(_blocks(V), n)
+        # the gradient, after the loss; the columns of padding stay zero (nothing writes them)
+        self.logits = torch.zeros(n, ld, device="cuda")[:, :head.V]
+        self.gq, self.gs = u8(n, ld), f32(_blocks(ld), n)
         self.dy = f32(n, hs)
         self.dx = torch.empty(n, hs, dtype=torch.bfloat16, device="cuda")
         self.dgamma, self.dbeta = f32(hs), f32(hs)
@@ -73,31 +75,31 @@ class Step:
         h, n = self.head, self.n
         vl.vl_layernorm_fwd_bf16(x, h.hs, n, h.hs, gamma, beta, eps, self.y, h.hs, self.mu, self.rstd)
         vl.vl_quant_fp8_rows_bf16(self.y, h.hs, n, h.hs, self.yq, self.ys)
-        vl.vl_gemm_fp8_tn(self.yq, self.ys, *h.plane, self.logits, n, h.V, h.hs, h.V)
+        vl.vl_gemm_fp8_tn(self.yq, self.ys, *h.plane, self.logits, n, h.V, h.hs, h.ld)
         return self.logits
 
     def backward(self, x, gamma):
         """From the gradient that a loss left in the logits' place: dx, dgamma, dbeta."""
         h, n = self.head, self.n
-        vl.vl_quant_fp8_rows(self.logits, h.V, n, h.V, self.gq, self.gs)
-        vl.vl_gemm_fp8_tn(self.gq, self.gs, *h.back, self.dy, n, h.hs, h.V, h.hs)
+        vl.vl_quant_fp8_rows(self.logits, h.ld, n, h.ld, self.gq, self.gs)
+        vl.vl_gemm_fp8_tn(self.gq, self.gs, *h.back, self.dy, n, h.hs, h.ld, h.hs)
         vl.vl_layernorm_bwd_bf16(self.dy, h.hs, x, h.hs, n, h.hs, gamma, self.mu, self.rstd, self.dx, h.hs, self.dgamma,
                                  self.dbeta, workspace=self.norm_ws)
         return self.dx, self.dgamma, self.dbeta
 
     def policy(self, x, gamma, beta, actions, old_logp, ref_logp, adv, weight, clip=(0.2, 0.2), kl_coef=0.04):
         """A policy step: total [1] and per-row loss, logp, kl stay in the buffers; returns the gradients."""
-        s, V = self.logits_of(x, gamma, beta), self.head.V
-        vl.vl_policy_loss(s, V, self.n, V, actions, old_logp, ref_logp, adv, weight, *clip, kl_coef, 1.0, s, V,
+        s, V, ld = self.logits_of(x, gamma, beta), self.head.V, self.head.ld
+        vl.vl_policy_loss(s, ld, self.n, V, actions, old_logp, ref_logp, adv, weight, *clip, kl_coef, 1.0, s, ld,
                           self.loss, self.logp, self.kl, self.total)
         return self.backward(x, gamma)
 
     def preference(self, x, gamma, beta, labels, weight, seq_start, npairs, ref_logp, loss, margin, seq_logp,
                    strength=0.1, kind=0):
         """A preference step over npairs pairs (kind: 0 sigmoid, 1 squared, 2 hinge); returns the gradients."""
-        s, V = self.logits_of(x, gamma, beta), self.head.V
-        vl.vl_preference_loss(s, V, self.n, V, labels, weight, seq_start, npairs, ref_logp, strength, 0.0, kind,
-                              1.0 / npairs, s, V, loss, margin, seq_logp, self.total, workspace=self.pair_ws)
+        s, V, ld = self.logits_of(x, gamma, beta), self.head.V, self.head.ld
+        vl.vl_preference_loss(s, ld, self.n, V, labels, weight, seq_start, npairs, ref_logp, strength, 0.0, kind,
+                              1.0 / npairs, s, ld, loss, margin, seq_logp, self.total, workspace=self.pair_ws)
         return self.backward(x, gamma)
 
 

@@ -459,7 +459,10 @@ VL_API vl_status vl_layernorm_bwd_bf16(const void* dy, int dy_f32, int64_t lddy,
  *   A [M][K], B [N][K] e4m3 bytes, row-major, 16-byte aligned, K a multiple of 16;
  *   sa [ceil(K/128)][M], sb [ceil(N/128)][ceil(K/128)] fp32; D [M][ldd] fp32.
  * With a frozen head: logits = hidden . W^T; and dx = g . Wt^T over the transposed plane Wt
- * [hs][V], whose 128 x 128 blocks have the transposed scales.
+ * [hs][V], whose 128 x 128 blocks have the transposed scales.  On the way back V is the contraction: a
+ * vocabulary that is no multiple of 16 is padded to Vp, the next one.  Logits and gradient get rows of
+ * stride Vp whose columns past V are zeroed once (neither the product forward, N = V and ldd = Vp, nor the
+ * losses write them), the gradient is quantised with K = Vp, and Wt is [hs][Vp] with zeros past V.
  *
  * The quantisers: over each block, scale = max(amax, 2^-100) * fp32(1 / 448), rounded to fp32,
  * and q = x / scale (an fp32 division) rounded to the nearest e4m3, ties to even, at most 448.  A NaN stays NaN, an infinity
