@@ -131,3 +131,40 @@ def test_no_kept_workspace_in_a_captured_call():
     assert before == set(vl._stream_ws)
     for k, t in zip(("grad", "loss", "margin", "seq"), out):
         assert torch.equal(t, want[k]), k
+
+
+@pytest.mark.parametrize("where", ["another", "default"])
+def test_topk_workspace_of_another_stream(where):
+    """The cached buffer of the top-k calls: allocated on the call's stream, an outgrown one kept."""
+    torch = H.torch_cuda()
+    from top_kl_distill_gb300 import vloss as vl
+    n, V, k = 300, 40000, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(n, V, device="cuda", generator=g)
+    need = vl.vl_topk_workspace_bytes(n, V, k)
+    want_p, want_i = torch.topk(x, k, dim=1)
+    want_p = torch.softmax(want_p, 1)
+    side = torch.cuda.Stream()
+    current, s = (torch.cuda.default_stream(), side.cuda_stream) if where == "another" else (side, 0)
+    held = vl._topk_ws.pop(0, None)                          # (kept alive: it may be in a graph)
+    ids, probs = torch.empty(n, k, dtype=torch.int32, device="cuda"), torch.empty(n, k, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(current):
+        other = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+        busy = torch.empty(need, dtype=torch.uint8, device="cuda")
+        at = busy.data_ptr()
+        torch.cuda.synchronize()
+        for _ in range(100):
+            other.fill_(1)
+            busy.fill_(0)
+        del busy
+        vl.vl_topk_rows(x, V, n, V, k, 0, n, ids, probs, stream=s)
+    first = vl.topk_workspace(1, 0)
+    torch.cuda.synchronize()
+    assert first.data_ptr() >= at + need or at >= first.data_ptr() + first.numel()
+    assert torch.equal(ids.long(), want_i) and torch.allclose(probs, want_p, rtol=1e-5)
+    grown = vl.topk_workspace(2 * first.numel(), 0)
+    assert grown.data_ptr() != first.data_ptr() and vl.topk_workspace(1, 0) is grown
+    assert any(t is first for t in vl._topk_ws[0])
+    del held

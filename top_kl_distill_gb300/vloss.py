@@ -266,16 +266,23 @@ def vl_topk_workspace_bytes(ntok, V, k) -> int:
 _topk_ws = {}
 
 
-def topk_workspace(nbytes, device=None):
+def _stream_of(dev, s):
+    """torch's stream of handle s (a null handle would make ExternalStream take a stream from torch's pool)."""
+    return _torch.cuda.ExternalStream(s, device=dev) if s else _torch.cuda.default_stream(dev)
+
+
+def topk_workspace(nbytes, device=None, stream=None):
     """A cached device buffer of at least `nbytes` for vl_topk_rows on `device` (grown on
-    demand).  One per device: calls that use it must not overlap on the GPU."""
-    import torch
+    demand).  One per device: calls that use it must not overlap on the GPU.  It is allocated on
+    the call's stream (a block freed on another may still be in use there), and an outgrown one
+    stays alive: queued work or a captured graph may still use it."""
+    torch = _torch or _load_torch()
     dev = torch.cuda.current_device() if device is None else int(device)
-    ws = _topk_ws.get(dev)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(int(nbytes), dtype=torch.uint8, device=f"cuda:{dev}")
-        _topk_ws[dev] = ws
-    return ws
+    kept = _topk_ws.setdefault(dev, [])
+    if not kept or kept[-1].numel() < nbytes:
+        with torch.cuda.stream(_stream_of(dev, _stream(stream))):
+            kept.append(torch.empty(int(nbytes), dtype=torch.uint8, device=f"cuda:{dev}"))
+    return kept[-1]
 
 
 def vl_topk_rows(logits, ld, ntok, V, k, loss_start, loss_end, ids, probs, err=None, workspace="auto",
@@ -287,9 +294,9 @@ def vl_topk_rows(logits, ld, ntok, V, k, loss_start, loss_end, ids, probs, err=N
             raise ValueError("workspace: a tensor, an int address, None or 'auto'")
         need = vl_topk_workspace_bytes(max(1, loss_end - loss_start), V, k) if loss_end > loss_start else 0
         if need:
-            import torch
+            torch = _torch or _load_torch()
             dev = logits.device.index if isinstance(logits, torch.Tensor) else None
-            w = topk_workspace(need, dev)
+            w = topk_workspace(need, dev, stream)
             workspace, workspace_bytes = w.data_ptr(), need
         else:
             workspace, workspace_bytes = None, 0
@@ -321,15 +328,15 @@ def vl_watchdog_flag(device: int = 0, clear: bool = True) -> int:
 # ---------------------------------------------------------------- the vocabulary head
 
 
-def _buf(ws, nbytes_auto, logits_like):
+def _buf(ws, nbytes_auto, logits_like, stream=None):
     """(address, bytes) of a workspace argument: 'auto' (a cached buffer of nbytes_auto), a tensor,
     or (address, bytes)."""
     if isinstance(ws, str):
         if ws != "auto":
             raise ValueError("workspace: a tensor, an int address or 'auto'")
-        import torch
+        torch = _torch or _load_torch()
         dev = logits_like.device.index if isinstance(logits_like, torch.Tensor) else None
-        w = topk_workspace(nbytes_auto, dev)
+        w = topk_workspace(nbytes_auto, dev, stream)
         return w.data_ptr(), int(nbytes_auto)
     if isinstance(ws, tuple):
         return int(ws[0]), int(ws[1])
@@ -343,7 +350,7 @@ def vl_teacher_topk(hidden, hs, w, V, ntok, k, loss_start, loss_end, ids, probs,
     """hidden [ntok][hs] and w [V][hs]: torch.bfloat16 tensors (or int addresses).  With
     workspace='auto' a cached buffer for chunks of `chunk` rows."""
     rows = max(1, min(chunk, max(1, loss_end - loss_start)))
-    ws, nb = _buf(workspace, int(lib().vl_teacher_topk_workspace_bytes(rows, V, k)), hidden)
+    ws, nb = _buf(workspace, int(lib().vl_teacher_topk_workspace_bytes(rows, V, k)), hidden, stream)
     _check("vl_teacher_topk", lib().vl_teacher_topk(
         _ptr(hidden, "bf16", "hidden"), hs, _ptr(w, "bf16", "w"), V, ntok, k, loss_start, loss_end,
         _ptr(ids, "u32", "ids"), _ptr(probs, "f32", "probs"), _ptr(err, "i32", "err"), ws, nb, _stream(stream)))
@@ -354,7 +361,7 @@ def vl_head_kl(hidden, hs, w, wt, V, ntok, labels, tid, tp, k, coef, ce_coef, dx
     """The student's head step; hidden, w (and the transposed plane wt, or None) bf16
     tensors, dx fp32 [ntok][hs]."""
     rows = max(1, min(chunk, max(1, ntok)))
-    ws, nb = _buf(workspace, int(lib().vl_head_kl_workspace_bytes(rows, V)), hidden)
+    ws, nb = _buf(workspace, int(lib().vl_head_kl_workspace_bytes(rows, V)), hidden, stream)
     _check("vl_head_kl", lib().vl_head_kl(
         _ptr(hidden, "bf16", "hidden"), hs, _ptr(w, "bf16", "w"), _ptr(wt, "bf16", "wt"), V, ntok,
         _ptr(labels, "u32", "labels"),
@@ -400,8 +407,7 @@ def _ws(workspace, need, like, stream):
     s = _stream(stream)
     if s == _stream(None) and dev == torch.cuda.current_device():
         return _kept_ws(torch, dev, s, need)
-    # (a null handle would make ExternalStream take a stream from torch's pool)
-    with torch.cuda.stream(torch.cuda.ExternalStream(s, device=dev) if s else torch.cuda.default_stream(dev)):
+    with torch.cuda.stream(_stream_of(dev, s)):
         return _kept_ws(torch, dev, s, need)
 
 
