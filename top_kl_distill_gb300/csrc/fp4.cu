@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(192, 2)
             for (uint32_t gg = g > (uint32_t)C::STAGES ? g - C::STAGES : 0u; gg < g; ++gg)
                 wait_parity_drain(&S.full[gg % C::STAGES], (gg / C::STAGES) & 1u);
     } else if (warp == 1) {
+        pdl_wait_primary();              // no copy comes before: a wait for one would spend its limit on the work ahead
         uint32_t g = 0, tile = 0;
         bool stop = false;
         const uint64_t dw = sw128_desc(smem_u32(S.w[0])), dx = sw128_desc(smem_u32(S.x[0]));
@@ -546,6 +547,7 @@ __global__ void __launch_bounds__(384, 1)
         // (2048 x 32000 x 8192, bf16 out: 163 us; a warp that meets in each stage 174, twice 204; the tile's first stage told
         // apart within the loop 1 to 3% more).  Every turn from copies to MMAs costs: copies a stage ahead, all before an
         // MMA (183) or four after each (192), are slower than all of a stage's together.
+        pdl_wait_primary();              // no copy comes before: a wait for one would spend its limit on the work ahead
         if (elect_one()) {
             uint32_t g = 0, tile = 0;
             bool stop = false;

@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(192, 2)
             for (uint32_t gg = g > (uint32_t)C::STAGES ? g - C::STAGES : 0u; gg < g; ++gg)
                 wait_parity_drain(&S.full[gg % C::STAGES], (gg / C::STAGES) & 1u);
     } else if (warp == 1) {
+        pdl_wait_primary();              // no copy comes before: a wait for one would spend its limit on the work ahead
         uint32_t g = 0;
         bool stop = false;
         const uint64_t dw = sw128_desc(smem_u32(S.w[0])), dx = sw128_desc(smem_u32(S.x[0]));
