@@ -537,17 +537,18 @@ VL_API vl_status vl_gemm_fp4_tn_bf16(const uint8_t* A, const uint8_t* sfa, const
  * Accepted and drawn tokens are then distributed as the target's own.  draft = NULL: the drafter proposes without
  * probabilities, q_j is 1 at its token.  temperature 0: greedy, a token is accepted if it is the target's largest
  * (the lowest column of equal ones), and the next one is that; u, pick and draft are not used.  k = 0 draws from the target.
- *   target [ndraft + nseq][ldt], draft [ndraft][ldd] (nullable) fp32 or bf16; -inf bans a column
+ *   target [ndraft + nseq][ldt], draft [ndraft][ldd] (nullable) fp32 or bf16; -inf bans a column, as does any number far below
+ *       the row's largest (-1e10, the type's lowest)
  *   seq_start [nseq + 1] int64 (device), 0 to ndraft, not falling       drafted [ndraft] u32    u [ndraft], pick [nseq] fp32 in [0, 1)
  *   temperature [nseq] fp32, 0 or in [1e-6, 1e6] (nullable: 1)
  *   tokens [ndraft + nseq] u32: from place seq_start[i] + i the accepted tokens, the next one, then 0xFFFFFFFF
  *   accepted [nseq] int32: how many were accepted
  *   logp [ndraft + nseq] fp32 (nullable): ln p of each of these tokens (greedy: at temperature 1), 0 past the last
  * Data errors, counted into *err (nullable) once a sequence: a drafted token >= V is refused; a row of target or draft
- * that is reached and has no softmax (a NaN, +inf, or nothing but -inf), or a temperature out of range, ends the sequence there with 0xFFFFFFFF
+ * that is reached and has no softmax (a NaN, +inf, or no column that is not banned), or a temperature out of range, ends the sequence there with 0xFFFFFFFF
  * as its next token.  Rows after the first refused token are not read.  A sequence's result does not depend on the others.
- * V is at most 2^30, a logit's magnitude 2^30 times the temperature (beyond it a row may have no softmax).  Outputs may not
- * overlap inputs.
+ * V is at most 2^30; the magnitude of a row's largest logit 2^30 times the temperature (beyond it a row may have no softmax).
+ * Outputs may not overlap inputs.
  */
 #define VL_VERIFY_MAX_SEQS (1LL << 24)
 VL_API vl_status vl_verify_draft(const float* target, int64_t ldt, const float* draft, int64_t ldd, int64_t V,

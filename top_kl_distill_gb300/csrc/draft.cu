@@ -16,7 +16,9 @@
 //
 // Statistics are in units of log2: m2 is the largest x sc, sc = log2(e) / temperature, rounded to fp32, and only a
 // reference: with x sc - m2 in one fma (its error is half an ulp of the difference, nothing near the top) the sums are
-// right relative to it whatever it was rounded by.  It would have to be off by 2^126 to lose them: x sc near 2^32.
+// right relative to it whatever it was rounded by.  It would have to be off by 2^126 to lose them: x sc near 2^32.  So a
+// reference is never below kLow: where a lane's columns are all masked, by -inf or by a number as low as the type has, each
+// is nothing next to it.  A row without anything else has the sum 0, and no softmax.
 //
 // 256 sequences of 8 drafted tokens over 128256 bf16 columns: 130 us, 546 MB read (4.2 TB/s; 490 MB are the rows that count);
 // 32 of 5: 27 us; one of 4 over 32000 fp32: 9.7.  A sweep's end (cluster barrier, decision) is 2 to 3 us in which its CTAs
@@ -45,6 +47,7 @@ constexpr int MAX_PER = 8;               // positions a sweep
 constexpr int ROWS = 2 * MAX_PER + 1;
 constexpr uint32_t kNone = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLow = -2147483648.f;    // half an ulp of what is above is 64 at most
 
 struct Smem {
     float2 part[2][ROWS][MAX_SEGS];      // (m2, sum of 2^(x sc - m2)) of a segment; by sweep, in turn
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) verify(const VerifyPar
             const T* row = row_of(r);
             int c0 = g * seg - shift_of(row);
             a.load(row, c0, V, lane, true);
-            float m2 = -INFINITY, z = 0.f, top = -INFINITY;
+            float m2 = kLow, z = 0.f, top = -INFINITY;
             int at = 0x7fffffff;
             // One piece, the next one's loads before its arithmetic.  The two take turns by name: a copy would wait for the
             // loads (151 us against 131 for 256 sequences of 8 over 128256 bf16 columns).
@@ -255,13 +258,12 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) verify(const VerifyPar
                     at = cur.find(t, here_c0, lane);
                     top = t;
                 }
-                const float nm = fmaxf(m2, t * sc), ref = nm == -INFINITY ? 0.f : nm;
-                // z of nothing yet: 0, or NaN
-                z = (m2 == -INFINITY ? z : z * ex2(m2 - ref)) + cur.sum_exps(ref, sc);
+                const float nm = fmaxf(m2, t * sc);
+                z = z * ex2(m2 - nm) + cur.sum_exps(nm, sc);
                 m2 = nm;
                 if (last) {
                     const float all = warp_max(m2);
-                    z = warp_sum(m2 == -INFINITY ? z : z * ex2(m2 - all));
+                    z = warp_sum(z * ex2(m2 - all));
                     if (lane < csize) st_cluster_f32x2(map_to_rank(&S.part[buf][here_r][here_g], lane), all, z);
                     if (greedy) {
                         const float high = warp_max(top);
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) verify(const VerifyPar
                         top = -INFINITY;
                         at = 0x7fffffff;
                     }
-                    m2 = -INFINITY;
+                    m2 = kLow;
                     z = 0.f;
                 }
                 return more;
@@ -291,12 +293,12 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) verify(const VerifyPar
             }
         cluster_sync_all();
         for (int r = warp; r < np + nq; r += WARPS) {
-            float m2 = -INFINITY, z = 0.f;
+            float m2 = kLow, z = 0.f;
             for (int g = lane; g < nseg; g += 32) m2 = fmaxf(m2, S.part[buf][r][g].x);
             m2 = warp_max(m2);
             for (int g = lane; g < nseg; g += 32) {
                 const float2 p = S.part[buf][r][g];
-                z += p.x == -INFINITY ? p.y : p.y * ex2(p.x - m2);
+                z += p.y * ex2(p.x - m2);
             }
             z = warp_sum(z);
             if (lane == 0) {
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) verify(const VerifyPar
             float lp = 0.f;
             if (lane < np) {
                 const float m = S.rm[lane], z = S.rz[lane];
-                bool fine = sane && m > -INFINITY && z > 0.f && z < INFINITY;
+                bool fine = sane && z > 0.f && z < INFINITY;
                 if (j0 + lane >= k) {
                     verdict = 2;
                 } else {
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) verify(const VerifyPar
                         verdict = d == (uint32_t)S.rat[lane] ? 0 : 1;
                     } else if (with_q) {
                         const float qm = S.rm[np + lane], qz = S.rz[np + lane];
-                        fine = fine && qm > -INFINITY && qz > 0.f && qz < INFINITY;
+                        fine = fine && qz > 0.f && qz < INFINITY;
                         verdict = S.u[buf][lane] < ex2(x2 - fmaf(S.yd[buf][lane], sc, -qm)) * (qz / z) ? 0 : 1;
                     } else {
                         verdict = S.u[buf][lane] < ex2(x2) / z ? 0 : 1;
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) verify(const VerifyPar
         if (!residual && warp == 0) {
             for (int g = lane; g < nseg; g += 32) {
                 const float2 p = S.part[buf][r][g];
-                S.sum[g] = p.x == -INFINITY ? 0.f : p.y * ex2(p.x - m) * inv;
+                S.sum[g] = p.y * ex2(p.x - m) * inv;
             }
             __syncwarp();
             if (out >= 0) {
