@@ -540,6 +540,7 @@ VL_API vl_status vl_gemm_fp4_tn_bf16(const uint8_t* A, const uint8_t* sfa, const
  *   target [ndraft + nseq][ldt], draft [ndraft][ldd] (nullable) fp32 or bf16; -inf bans a column, as does any number far below
  *       the row's largest (-1e10, the type's lowest)
  *   seq_start [nseq + 1] int64 (device), 0 to ndraft, not falling       drafted [ndraft] u32    u [ndraft], pick [nseq] fp32 in [0, 1)
+ *       (1 too, as rounding a number below it may give)
  *   temperature [nseq] fp32, 0 or in [1e-6, 1e6] (nullable: 1)
  *   tokens [ndraft + nseq] u32: from place seq_start[i] + i the accepted tokens, the next one, then 0xFFFFFFFF
  *   accepted [nseq] int32: how many were accepted

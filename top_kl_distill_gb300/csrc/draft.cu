@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) verify(const VerifyPar
             if (lane == at) {
                 S.pick_seg = g1;
                 S.goal = fmax(goal - before, 0.0);
-                S.whole = !(total > 0.0);          // p and q alike to the last bit: any draw from p will do
+                S.whole = !(total > 0.0);          // nothing is left (p and q alike, p all on the token refused): drawn from p
             }
         }
         __syncthreads();
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) verify(const VerifyPar
             float e = 0.f;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                if (!in || c0 + lane * N + j == out) w[j] = 0.f;
+                if (!in || (c0 + lane * N + j == out && !whole)) w[j] = 0.f;
                 e += w[j];
             }
             float incl = e;
