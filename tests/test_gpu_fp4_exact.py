@@ -1,0 +1,166 @@
+"""The 4-bit product over operands whose sums are exact in fp32, at every kernel and every way K is taken in parts.
+
+Values of e2m1 without zeros, block scales 0.5, 1 and 2, row scales and alpha powers of two: products are steps of 2^-4, sums stay
+below 2^20, so that fp32 holds each of them in any order and D is the exact result (rounded once in bf16).  A column of K that is
+lost, counted twice or given another's scale then changes D, however long K is: the comparison is of bits.
+
+Which kernel a shape runs is decided by its sizes and the number of SMs; the tests name the kernel that they are for, and check
+by its name that it ran.
+"""
+import numpy as np
+import pytest
+
+from oracle import draft_oracle as O
+from tests import gpu_harness as H
+
+pytestmark = pytest.mark.gpu
+
+
+def operands(M, N, K, fmt, seed):
+    """(A, B) as (codes, block scales, row scales) and what they stand for (fp64, on the GPU)."""
+    torch = H.torch_cuda()
+    g = np.random.default_rng(seed)
+    out = []
+    for m in (M, N):
+        c = (g.integers(1, 8, (m, K), dtype=np.uint8) | g.integers(0, 2, (m, K), dtype=np.uint8) << 3)
+        nb = -(-K // O.BLOCK[fmt])
+        s = g.choice(np.uint8([0x30, 0x38, 0x40] if fmt == O.NV else [126, 127, 128]), (m, nb))
+        r = np.ldexp(np.float32(1), g.integers(-2, 3, m)) if fmt == O.NV else np.ones(m, np.float32)
+        v = torch.from_numpy(O.E2M1[c & 7].astype(np.float32)).cuda()
+        v *= torch.from_numpy(1 - 2 * (c >> 3).astype(np.float32)).cuda()
+        v *= torch.from_numpy(O.scale_value(s, fmt).astype(np.float32)).cuda().repeat_interleave(O.BLOCK[fmt], 1)[:, :K]
+        out.append((c, s, r, v.double()))
+    return out
+
+
+def packed(rows, fmt):
+    c, s, r, _ = rows
+    return [H.dev(O.pack(c)), H.dev(tiles(s)), H.dev(r) if fmt == O.NV else None]
+
+
+def tiles(s):
+    """As the oracle's `tile`, with NaN scales for the rows past the last, in whole arrays."""
+    m, nb = s.shape
+    mt, kt = -(-m // 128), -(-nb // 4)
+    p = np.full((mt * 128, kt * 4), 0x7F, np.uint8)
+    p[:m] = 0
+    p[:m, :nb] = s
+    return np.ascontiguousarray(p.reshape(mt, 4, 32, kt, 4).transpose(0, 3, 2, 1, 4)).reshape(-1)
+
+
+def names(call):
+    """Names of the kernels that a call runs."""
+    torch = H.torch_cuda()
+    for _ in range(3):                                           # a process's first trace may come back empty
+        with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as p:
+            call()
+            torch.cuda.synchronize()
+        ran = [e.name for e in p.events()]
+        if any("fp4_gemm" in r for r in ran):
+            return ran
+    return []
+
+
+def check(M, N, K, fmt, bf16=False, pad=0, off=0, alpha=0.5, kernel=None):
+    torch = H.torch_cuda()
+    from top_kl_distill_gb300 import vloss as vl
+    a, b = operands(M, N, K, fmt, 7 * M + N + K)
+    assert float((a[3].abs() @ b[3].abs().t()).max()) < 2 ** 20
+    want = (a[3] @ b[3].t()) * (alpha * torch.from_numpy(a[2].astype(np.float64)).cuda()[:, None] * torch.from_numpy(b[2]).cuda())
+    dt, ld = torch.bfloat16 if bf16 else torch.float32, N + pad
+    buf = torch.full((off + M * ld + 8,), 5.0, device="cuda", dtype=dt)
+    D, ops = buf[off:off + M * ld], packed(a, fmt) + packed(b, fmt)
+    torch.cuda.synchronize()
+
+    def call():
+        (vl.vl_gemm_fp4_tn_bf16 if bf16 else vl.vl_gemm_fp4_tn)(*ops, D, M, N, K, ld, fmt, alpha)
+
+    call()
+    torch.cuda.synchronize()
+    got = D.view(M, ld)
+    off_by = got[:, :N] != want.float().to(dt)
+    assert not off_by.any(), (M, N, K, fmt, int(off_by.sum()), off_by.nonzero()[:4].tolist())
+    assert (got[:, N:] == 5).all() and (buf[:off] == 5).all() and (buf[off + M * ld:] == 5).all()
+    if kernel is not None:
+        ran = names(call)
+        if not ran:
+            pytest.skip("no kernel names to be had here (the results are right)")
+        assert any(kernel in r.replace(" ", "") for r in ran), (kernel, ran)
+
+
+@pytest.mark.parametrize("K", [256 * 8, 256 * 16, 256 * 32 + 1, 256 * 33, 9000 - 8 * 16 + 3])
+@pytest.mark.parametrize("M", [1, 5, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("fmt", [O.NV, O.MX])
+def test_few_rows_in_parts(M, K, fmt):
+    """Up to 64 rows and few weight rows: K in two, four and eight parts, ragged in K and in the weight's rows."""
+    for N in (130, 1000):
+        check(M, N, K, fmt, kernel="fp4_gemm<%d,%d>" % (16 if M <= 16 else 32 if M <= 32 else 64, fmt))
+    check(M, 77, K, fmt, bf16=True, pad=1)
+
+
+@pytest.mark.parametrize("M", [3, 24, 50])
+@pytest.mark.parametrize("fmt", [O.NV, O.MX])
+def test_few_rows_several_tiles_a_cta(M, fmt):
+    check(M, 80001, 600, fmt)
+    check(M, 80002, 300, fmt, bf16=True)
+
+
+@pytest.mark.parametrize("fmt", [O.NV, O.MX])
+@pytest.mark.parametrize("K", [256 * 8, 256 * 9 + 40, 9000, 20000])
+def test_pairs_in_two_parts(K, fmt):
+    """K in two parts over a cluster of two pairs, each width."""
+    for M, N, nt in ((70, 300, 128), (128, 700, 128), (300, 1100, 128), (180, 9001, 192), (230, 9001, 256), (250, 9001, 256)):
+        check(M, N, K, fmt, kernel="fp4_gemm_pairs<%d,%d,false>" % (nt, fmt) if K == 20000 else None)
+
+
+@pytest.mark.parametrize("M,N,K,nt,copies", [(250, 30000, 2050, 256, False), (250, 30001, 2800, 256, False), (1010, 19001, 2300, 256, False),
+                                             (250, 30000, 2800, 256, True), (2000, 9000, 4000, 256, True), (700, 20001, 1000, 192, False),
+                                             (700, 40001, 256, 192, False), (190, 40000, 2600, 192, True), (513, 20008, 2600, 192, True),
+                                             (100, 40001, 700, 128, False), (100, 40000, 2600, 128, True)])
+@pytest.mark.parametrize("fmt", [O.NV, O.MX])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_pairs_several_tiles(M, N, K, nt, copies, fmt, bf16):
+    """More tiles than pairs, so that accumulators change hands: each width, D by plain stores and by TMA, ragged ends."""
+    check(M, N, K, fmt, bf16, pad=8 if M > 600 else 0, kernel="fp4_gemm_pairs<%d,%d,%s>" % (nt, fmt, "true" if copies else "false"))
+
+
+@pytest.mark.parametrize("short", range(9))
+@pytest.mark.parametrize("bf16", [False, True])
+def test_rows_that_end_anywhere(short, bf16):
+    """Rows of D that begin at 16 bytes and end inside them: what lies behind a row stays as it was (what is behind the weight's
+    last row has NaN scales here)."""
+    for M, N in ((100, 24000), (190, 24000), (250, 30016)):
+        check(M, N - short, 2600, O.NV, bf16, pad=short)
+
+
+@pytest.mark.parametrize("off,pad", [(1, 0), (2, 2), (4, 4), (8, 1)])
+@pytest.mark.parametrize("fmt", [O.NV, O.MX])
+def test_pairs_at_any_place(off, pad, fmt):
+    for M, K in ((250, 2800), (190, 300), (70, 300)):
+        for bf16 in (False, True):
+            check(M, 21000, K, fmt, bf16, pad=pad, off=off)
+
+
+@pytest.mark.parametrize("fmt", [O.NV, O.MX])
+def test_every_remainder_of_rows(fmt):
+    for M in range(1, 34):
+        check(M, 200, 600, fmt)
+    for M in range(120, 137):
+        check(M, 520, 600, fmt, bf16=M % 2 == 0)
+    for M in range(250, 262):
+        check(M, 9000, 300, fmt, bf16=M % 2 == 0)
+
+
+@pytest.mark.parametrize("fmt", [O.NV, O.MX])
+def test_every_remainder_of_k(fmt):
+    for K in range(1, 300, 1 if fmt == O.NV else 3):
+        check(4, 130, K, fmt)
+    for K in range(1, 300, 7):
+        check(80, 130, K, fmt)
+
+
+@pytest.mark.parametrize("M,N", [(1, 40), (5, 130), (40, 300), (64, 128), (140, 300), (300, 520)])
+@pytest.mark.parametrize("K", [32000, 32003, 50257])
+@pytest.mark.parametrize("fmt", [O.NV, O.MX])
+def test_the_vocabulary_as_the_contraction(M, N, K, fmt):
+    check(M, N, K, fmt, bf16=M == 5)

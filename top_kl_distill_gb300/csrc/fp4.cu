@@ -759,7 +759,8 @@ cudaError_t go(const Fp4Gemm& G, GemmParams P, int dev, int sms, cudaStream_t st
     return launch_cluster(fp4_gemm<NT, FMT>, ctas, 192, smem, P.splits, st, tw, tx, P);
 }
 
-// Stages of K from which on D goes by TMA, where its rows begin at 16 bytes: the copies are the slower way, paced by their one
+// Stages of K from which on D goes by TMA, where its rows begin and end at 16 bytes (a copy that is cut off at a row's end writes
+// whole blocks of 16 bytes, past it): the copies are the slower way, paced by their one
 // buffer a warp, and leave the loads alone, so that a tile that takes longer than its epilogue hides them.  (2048 x 32000
 // fp32, us by TMA and by plain stores: K = 2048 79 and 70, 2560 85 and 84 (MX 78 and 81), 2816 86 and 90, 4096 100 and 115;
 // bf16 62 and 63, 74 and 76, 71 and 77, 90 and 103.  2048 x 128256 x 4096: 404 and 430.  With two buffers 403 against 390
@@ -799,7 +800,7 @@ cudaError_t pair_go(const Fp4Gemm& G, GemmParams P, int splits, int dev, int sms
     const int bytes = P.bf16 ? 2 : 4;
     P.splits = splits;
     const bool copies = splits == 1 && P.nk >= COPY_STAGES && reinterpret_cast<uintptr_t>(G.d) % 16 == 0 &&
-                        G.ldd * bytes % 16 == 0 && G.ldd < (1ll << 36);
+                        G.ldd * bytes % 16 == 0 && G.N * bytes % 16 == 0 && G.ldd < (1ll << 36);
     return copies ? pair_launch<NT, FMT, true>(G, P, dev, sms, st) : pair_launch<NT, FMT, false>(G, P, dev, sms, st);
 }
 

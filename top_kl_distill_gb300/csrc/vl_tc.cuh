@@ -45,7 +45,7 @@ __device__ __forceinline__ void tma_load_1cta(void* dst, const CUtensorMap* map,
 }
 
 // A box of shared memory to the in-range place (x, y), as a group of this thread's, after its and the warp's writes of it
-// were fenced.  What lies past the edges is not written.
+// were fenced.  What lies past the edges is not written, but for the rest of the 16 bytes in which a row ends.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
                  :: "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
