@@ -504,7 +504,8 @@ VL_API vl_status vl_gemm_fp8_tn(const uint8_t* A, const float* sa, const uint8_t
  * M is at most 2^31, K 2^30; buffers may not overlap.
  *
  * vl_gemm_fp4_tn: D[m][n] = alpha * ra[m] * rb[n] * sum over k of (qa sa)[m][k] (qb sb)[n][k], in fp32 (_bf16: rounded once
- * when written).  Products are exact, sums fp32 in the tensor cores; A [M][Kp/2], B [N][Kp/2] with scales as above,
+ * when written; the factors in an order that keeps what is between them in fp32 where the result is, for alpha 0 or of magnitude
+ * 2^-100 upwards).  Products are exact, sums fp32 in the tensor cores; A [M][Kp/2], B [N][Kp/2] with scales as above,
  * D [M][ldd].  K is any length from 1.  Logits from hidden rows and a head plane W [V][hs]; and dx = g . Wt^T over the transposed
  * plane Wt [hs][V], quantised by itself (its blocks run along V). 
  */

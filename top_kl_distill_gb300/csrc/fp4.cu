@@ -19,10 +19,13 @@
 #include "vl_fp4.h"
 #include "vl_internal.h"
 #include "vl_launch.h"
+#include "vl_pair.cuh"
 #include "vl_rowio.cuh"
 #include "vl_tc.cuh"
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 namespace vl {
@@ -94,29 +97,52 @@ struct GemmParams {
     int nk, tiles_k;          // stages; tiles of scales along K
     int mmas;                 // MMAs of 64 columns that K takes
     int splits;               // parts that K is taken in, by the CTAs (pairs) of a cluster: each has one tile then
-    float alpha;
+    float alpha, am;          // alpha = am 2^ea
+    int ea;
 };
 
-// Sixteen columns of the accumulator times rx (their row scales, in shared memory) and sn (this lane's, with alpha).
-__device__ __forceinline__ void scale16(float (&y)[16], const uint32_t (&v)[16], const float* rx, float sn) {
+// A lane's factors: D = ((v p) rx) q, v the sum (0, or 2^-20 to 2^53 in NV), rx the scale of a row of A, p q = rb alpha.
+// With p = 1 nothing on the way leaves fp32 that the result does not, if all rx are in 2^-64 to 2^64 and rb alpha is in fp32.
+// Where a row's is not (a product is `far` then) or a lane's is not, q is a power of two that leaves p in 2^-100 to 2^71: then
+// neither v p nor that times rx does.  (In fp64 on a path of their own such tiles cost the others 1 to 8%: whatever stands beside
+// the epilogue's one path makes it slower.  A second factor for the rows too, beside theirs in shared memory: 2 to 5%.)
+struct Lane {
+    float p, q;
+};
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ bool beyond(float rx) {
+    const float a = fabsf(rx);
+    return (a > 0.f && a < 5.421010862427522e-20f) || (a > 1.8446744073709552e19f && a < INFINITY);
+}
+// alpha = am 2^ea
+__device__ __forceinline__ Lane lane_scale(float rn, float alpha, float am, int ea, bool far) {
+    const float s = rn * am;
+    const int e = (int)(__float_as_uint(s) >> 23 & 255u) - 127 + ea, k = e > 70 ? min(e - 70, 126) : e < -100 ? max(e + 100, -126) : 0;
+    const int half = (ea - k) / 2;
+    return far || e > 120 || e < -120 ? Lane{s * pow2(half) * pow2(ea - k - half), pow2(k)} : Lane{1.f, rn * alpha};
+}
+
+// Arithmetic on a loaded value stays behind this place, where it may wait for the load.
+__device__ __forceinline__ void hold(float& r) { asm volatile("" : "+f"(r)); }
+
+// Sixteen columns of the accumulator, scaled; rx in shared memory.
+__device__ __forceinline__ void scale16(float (&y)[16], const uint32_t (&v)[16], const float* rx, Lane s) {
+    const uint64_t p = both(s.p), q = both(s.q);
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
         const float4 r = *reinterpret_cast<const float4*>(rx + j);
-        y[j] = __uint_as_float(v[j]) * r.x * sn;
-        y[j + 1] = __uint_as_float(v[j + 1]) * r.y * sn;
-        y[j + 2] = __uint_as_float(v[j + 2]) * r.z * sn;
-        y[j + 3] = __uint_as_float(v[j + 3]) * r.w * sn;
+        const uint64_t lo = mul2(pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), p);
+        const uint64_t hi = mul2(pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), p);
+        unpack2(mul2(mul2(lo, pack2(r.x, r.y)), q), y[j], y[j + 1]);
+        unpack2(mul2(mul2(hi, pack2(r.z, r.w)), q), y[j + 2], y[j + 3]);
     }
 }
 
-// Sixteen columns of the accumulator (rows m .. m + 15 of D, the first `rows` of them) of this lane's column n, scaled.
+// Sixteen scaled columns of the accumulator (rows m .. m + 15 of D, the first `rows` of them) of this lane's column n.
 // ALL: nothing of the warp's 32 x 16 is past the edges.  A store of the warp is one contiguous piece of a row; in bf16 neighbouring lanes swap values, so that it is two
 // rows' pieces of 4 bytes a lane.
 template <bool ALL>
-__device__ __forceinline__ void put16(const GemmParams& P, const uint32_t (&v)[16], const float* rx, float sn, int m, int rows,
-                                      int n, int lane) {
-    float y[16];
-    scale16(y, v, rx, sn);
+__device__ __forceinline__ void put16(const GemmParams& P, const float (&y)[16], int m, int rows, int n, int lane) {
     if (!P.bf16) {
         float* d = static_cast<float*>(P.d) + m * P.ldd + n;
 #pragma unroll
@@ -139,12 +165,10 @@ __device__ __forceinline__ void put16(const GemmParams& P, const uint32_t (&v)[1
     }
 }
 
-// The same by TMA, the warp's 32 columns from n0 on: 1 KB at a time (16 rows of bf16, 8 of fp32) through `buf`, which the copy
+// `put16` by TMA, the warp's 32 columns from n0 on: 1 KB at a time (16 rows of bf16, 8 of fp32) through `buf`, which the copy
 // before has to have left.
-__device__ __forceinline__ void copy16(const GemmParams& P, const CUtensorMap* td, uint8_t* buf, const uint32_t (&v)[16],
-                                       const float* rx, float sn, int m, int n0, int lane) {
-    float y[16];
-    scale16(y, v, rx, sn);
+__device__ __forceinline__ void copy16(const GemmParams& P, const CUtensorMap* td, uint8_t* buf, const float (&y)[16], int m,
+                                       int n0, int lane) {
     if (P.bf16) {
         if (lane == 0) tma_stores_read();
         __syncwarp();
@@ -176,18 +200,20 @@ __device__ __forceinline__ void copy16(const GemmParams& P, const CUtensorMap* t
 // `sides` warps share the columns; `step`: CTAs of a part.  (4 columns of a lane a store: a store of one is four times as
 // many to another SM, 8 us for 256 x 256 against 2.)
 template <int NT>
-__device__ __forceinline__ void join(const GemmParams& P, float4* ring, float* rx, uint32_t acc, int q, int side, int sides,
+__device__ __forceinline__ void join(const GemmParams& P, float4* ring, float* rx, int* far, uint32_t acc, int q, int side, int sides,
                                      int part, int step, int in_part, int n, int m0, int lane) {
     const int own = NT / P.splits;               // a multiple of 4
     acc += (uint32_t)(32 * max(q, 0)) << 16;
     // four columns of part p's for a part, in groups of four: [others][own / 4][128]
     auto place = [&](int from, int to, int c) { return ((from - (from > to)) * (own / 4) + c / 4) * 128 + 32 * q + lane; };
-    float sn = 1.f;
+    float rn = 1.f;
     if (q >= 0) {                                // all that the end reads from memory, before anyone waits for anyone
-        sn = (P.rw && n < P.N ? P.rw[n] : 1.f) * P.alpha;
+        rn = P.rw && n < P.N ? P.rw[n] : 1.f;
         for (int c = (4 * side + q) * 32 + lane; c < NT; c += 128 * sides) {
             const int m = m0 + part * own + c;
-            rx[c] = P.rx && c < own && m < P.M ? P.rx[m] : 1.f;
+            const float r = P.rx && c < own && m < P.M ? P.rx[m] : 1.f;
+            if (beyond(r)) *far = 1;
+            rx[c] = r;
         }
     }
     cluster_sync_all();
@@ -212,6 +238,7 @@ __device__ __forceinline__ void join(const GemmParams& P, float4* ring, float* r
     }
     cluster_sync_all();
     if (q < 0) return;
+    const Lane sn = lane_scale(rn, P.alpha, P.am, P.ea, *far);
     const bool all = own >= 16 && m0 + (part + 1) * own <= P.M && n - lane + 32 <= P.N;
 #pragma unroll 1
     for (int c = 16 * side; c < own; c += 16 * sides) {
@@ -236,9 +263,10 @@ __device__ __forceinline__ void join(const GemmParams& P, float4* ring, float* r
         }
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(s[j]);
+        scale16(s, v, rx + c, sn);
         const int m = m0 + part * own + c;
-        if (all) put16<true>(P, v, rx + c, sn, m, 16, n, lane);
-        else put16<false>(P, v, rx + c, sn, m, min(P.M - m, own - c), n, lane);
+        if (all) put16<true>(P, s, m, 16, n, lane);
+        else put16<false>(P, s, m, min(P.M - m, own - c), n, lane);
     }
 }
 
@@ -265,7 +293,7 @@ struct alignas(1024) Smem {
     uint64_t full[Cfg<NT, FMT>::STAGES], empty[Cfg<NT, FMT>::STAGES];
     uint64_t tfull[2], tempty[2], done;
     uint32_t tmem_base;
-    int abort;
+    int abort, far;                      // a wait ran out; rows' scales that `Lane` has to keep in range
 };
 
 template <int NT, int FMT>
@@ -288,7 +316,7 @@ __global__ void __launch_bounds__(192, 2)
             mbar_init(&S.tempty[b], 4);
         }
         mbar_init(&S.done, 1);
-        S.abort = 0;
+        S.abort = S.far = 0;
         fence_mbar_init_cluster();
     }
     if (warp == 1) {
@@ -376,10 +404,15 @@ __global__ void __launch_bounds__(192, 2)
         const int q = warp & 3;
         float* const rx = S.rx[warp - 2];
         uint32_t tile = 0;
+        bool far = false;
+        if (FMT == kNv && P.splits == 1) {
+            for (int i = lane; i < P.M; i += 32) far = far || beyond(P.rx[i]);
+            far = __any_sync(0xffffffffu, far);
+        }
         for (int t = first; t < tiles; t += stride, ++tile) {
             const uint32_t b = tile & 1u;
             const int n = t * 128 + 32 * q + lane;
-            const float sn = (P.rw && n < P.N ? P.rw[n] : 1.f) * P.alpha;
+            float rn = P.rw && n < P.N ? P.rw[n] : 1.f;
             __syncwarp();
             for (int i = lane; i < NT; i += 32) rx[i] = P.rx && i < P.M ? P.rx[i] : 1.f;
             __syncwarp();
@@ -390,6 +423,8 @@ __global__ void __launch_bounds__(192, 2)
             const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + b * NT;
             uint32_t v[2][16];
             tmem_ld16(acc, v[0]);
+            hold(rn);
+            const Lane sn = lane_scale(rn, P.alpha, P.am, P.ea, far);
 #pragma unroll
             for (int c = 0; c < NT / 16; ++c) {
                 tmem_wait16(v[c & 1]);
@@ -398,14 +433,16 @@ __global__ void __launch_bounds__(192, 2)
                     tc_fence_before();
                     if (lane == 0) mbar_arrive(&S.tempty[b]);
                 }
-                if (cols && 16 * c + 16 <= P.M) put16<true>(P, v[c & 1], rx + 16 * c, sn, 16 * c, 16, n, lane);
-                else if (16 * c < P.M) put16<false>(P, v[c & 1], rx + 16 * c, sn, 16 * c, P.M - 16 * c, n, lane);
+                float y[16];
+                scale16(y, v[c & 1], rx + 16 * c, sn);
+                if (cols && 16 * c + 16 <= P.M) put16<true>(P, y, 16 * c, 16, n, lane);
+                else if (16 * c < P.M) put16<false>(P, y, 16 * c, P.M - 16 * c, n, lane);
             }
         }
     }
     __syncwarp();
     if (P.splits > 1)
-        join<NT>(P, reinterpret_cast<float4*>(S.w), S.rxj, tmem, warp >= 2 ? warp & 3 : -1, 0, 1, part, 1, 0,
+        join<NT>(P, reinterpret_cast<float4*>(S.w), S.rxj, &S.far, tmem, warp >= 2 ? warp & 3 : -1, 0, 1, part, 1, 0,
                  first * 128 + 32 * (warp & 3) + lane, 0, lane);
     __syncwarp();
     tc_fence_before();
@@ -469,7 +506,7 @@ struct alignas(1024) PSmem {
     uint64_t tempty[2];                          // (leader) both CTAs' epilogues have read what the next MMAs overwrite
     uint64_t done;                               // every MMA issued has completed
     uint32_t tmem_base;
-    int abort;
+    int abort, far;                              // a wait ran out; rows' scales that `Lane` has to keep in range
 };
 
 // COPIES: D is written by TMA (both ways in one kernel: 0.4 to 1 us slower at 256 x 32000 x 2048, 15).
@@ -497,7 +534,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&S.tempty[b], 16);
         }
         mbar_init(&S.done, 1);
-        S.abort = 0;
+        S.abort = S.far = 0;
         fence_mbar_init_cluster();
     }
     __syncthreads();
@@ -610,13 +647,21 @@ __global__ void __launch_bounds__(384, 1)
         constexpr int CH = NT / 32, SH = C::SHARED / 32;       // a warp's chunks of 16 columns, and those shared
         float* const rx = S.rx[warp - 4];
         uint32_t tile = 0;
+        // asked once, of all rows: tile by tile even the question cost 1 to 5%
+        if (FMT == kNv && P.splits == 1) {
+            bool any = false;
+            for (int m = threadIdx.x - 128; m < P.M; m += 256) any = any || beyond(P.rx[m]);
+            if (any) S.far = 1;
+            named_sync(1, 256);
+        }
+        const bool far = S.far != 0;
         for (int t = cid; t < tiles; t += ncl, ++tile) {
             const uint32_t b = tile & 1u, acc = tmem + ((uint32_t)(32 * q) << 16) + b * C::ACC1;
             const int n = t / mt * 256 + mine + 32 * q + lane, m0 = t % mt * NT;
             // the shared chunks first: the first accumulator's last columns, the second's first
             const int sh0 = (b ? 0 : C::ACC1) + 16 * SH * side, own0 = (b ? C::SHARED : 0) + 16 * (CH - SH) * side;
             auto col = [&](int i) { return i < SH ? sh0 + 16 * i : own0 + 16 * (i - SH); };
-            const float sn = (P.rw && n < P.N ? P.rw[n] : 1.f) * P.alpha;
+            float rn = P.rw && n < P.N ? P.rw[n] : 1.f;
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < (CH + 1) / 2; ++i) {
@@ -628,12 +673,15 @@ __global__ void __launch_bounds__(384, 1)
             if (!wait_all(&S.tfull[b], (tile >> 1) & 1u, &S.abort)) break;
             if (P.splits > 1) break;
             tc_fence_after();
+            Lane sn;
             auto put = [&](int i, const uint32_t (&w)[16]) {
                 const int m = m0 + col(i);
+                float y[16];
+                scale16(y, w, rx + 16 * i, sn);
                 if constexpr (COPIES) {
-                    if (m < P.M && n - lane < P.N) copy16(P, &td, S.out[warp - 4], w, rx + 16 * i, sn, m, n - lane, lane);
-                } else if (cols && m + 16 <= P.M) put16<true>(P, w, rx + 16 * i, sn, m, 16, n, lane);
-                else if (m < P.M) put16<false>(P, w, rx + 16 * i, sn, m, P.M - m, n, lane);
+                    if (m < P.M && n - lane < P.N) copy16(P, &td, S.out[warp - 4], y, m, n - lane, lane);
+                } else if (cols && m + 16 <= P.M) put16<true>(P, y, m, 16, n, lane);
+                else if (m < P.M) put16<false>(P, y, m, P.M - m, n, lane);
             };
             uint32_t v[2][16];
             if constexpr (SH > 0) {
@@ -646,10 +694,14 @@ __global__ void __launch_bounds__(384, 1)
                 tc_fence_before();
                 if (lane == 0) arrive_cluster(tempty[b]);
                 tmem_ld16(acc + (uint32_t)col(SH), v[SH & 1]);
+                hold(rn);
+                sn = lane_scale(rn, P.alpha, P.am, P.ea, far);
 #pragma unroll
                 for (int i = 0; i < SH; ++i) put(i, s[i]);
             } else {
                 tmem_ld16(acc + (uint32_t)col(0), v[0]);
+                hold(rn);
+                sn = lane_scale(rn, P.alpha, P.am, P.ea, far);
             }
 #pragma unroll
             for (int i = SH; i < CH; ++i) {
@@ -666,7 +718,7 @@ __global__ void __launch_bounds__(384, 1)
     }
     __syncwarp();
     if (P.splits > 1)
-        join<NT>(P, reinterpret_cast<float4*>(S.w), S.rxj, tmem, warp >= 4 ? warp & 3 : -1, (warp - 4) >> 2, 2, part, 2, half,
+        join<NT>(P, reinterpret_cast<float4*>(S.w), S.rxj, &S.far, tmem, warp >= 4 ? warp & 3 : -1, (warp - 4) >> 2, 2, part, 2, half,
                  cid / mt * 256 + mine + 32 * (warp & 3) + lane, cid % mt * NT, lane);
     __syncwarp();
     tc_fence_before();
@@ -856,7 +908,9 @@ cudaError_t fp4_gemm_tn(const Fp4Gemm& G, cudaStream_t st) {
     P.nk = (int)((fp4_kp(G.K) + KE - 1) / KE);
     P.tiles_k = (int)fp4_tiles_k(G.K, G.fmt);
     P.mmas = (int)((G.K + 63) / 64);
-    P.alpha = G.alpha;
+    P.alpha = P.am = G.alpha;
+    P.ea = 0;
+    if (std::isfinite(G.alpha)) P.am = std::frexp(G.alpha, &P.ea);
     return G.fmt == kNv ? pick<kNv>(G, P, dev, sms, st) : pick<kMx>(G, P, dev, sms, st);
 }
 
