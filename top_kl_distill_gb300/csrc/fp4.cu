@@ -39,12 +39,9 @@ constexpr int SF_TILE = 512;             // 128 rows x 4 blocks of scales
 template <int FMT>
 constexpr int SF_TILES = FMT == kNv ? 4 : 2;                // tiles of scales a stage and 128 rows
 
-// The bounded wait of one thread; of a warp.
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, int* abort) {
-    return wait_parity<false>(bar, parity, abort, &g_watchdog);
-}
+// wait_parity by a whole warp: all lanes agree on whether it gave up.
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int* abort) {
-    return __all_sync(0xffffffffu, wait_one(bar, parity, abort));
+    return __all_sync(0xffffffffu, wait_parity<false>(bar, parity, abort, &g_watchdog));
 }
 
 // Instruction descriptor: A, B e2m1 (bits 7-9, 10-12 = 1), N >> 3, scales e4m3 or e8m0 (bit 23), M >> 4; K = 64.
@@ -620,14 +617,14 @@ __global__ void __launch_bounds__(384, 1)
                 const uint32_t odd = (uint32_t)(mi * NT % 128) / 32u, acc = tmem + (tile & 1u) * C::ACC1;
                 const uint32_t free = tile - (C::SHARED ? 1u : 2u);        // the tile whose columns these MMAs overwrite
                 uint32_t s = g % C::STAGES;
-                if ((int)free >= 0 && !wait_one(&S.tempty[free & 1u], (free >> 1) & 1u, &S.abort)) break;
-                if (!wait_one(&S.full[s], (g / C::STAGES) & 1u, &S.abort)) break;
+                if ((int)free >= 0 && !wait_parity<false>(&S.tempty[free & 1u], (free >> 1) & 1u, &S.abort, &g_watchdog)) break;
+                if (!wait_parity<false>(&S.full[s], (g / C::STAGES) & 1u, &S.abort, &g_watchdog)) break;
                 tc_fence_after();
                 scales(s);
                 multiply(s, acc, odd, min(4, P.mmas - 4 * kb0), std::false_type());
                 for (int kb = kb0 + 1; kb < kb1; ++kb) {
                     s = g % C::STAGES;
-                    if (!wait_one(&S.full[s], (g / C::STAGES) & 1u, &S.abort)) {
+                    if (!wait_parity<false>(&S.full[s], (g / C::STAGES) & 1u, &S.abort, &g_watchdog)) {
                         stop = true;
                         break;
                     }
