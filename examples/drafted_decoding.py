@@ -1,6 +1,8 @@
 """Drafted decoding at the vocabulary head, through the library's calls alone: a small student proposes tokens, its teacher
 looks at all of them in one pass and keeps what it would have said itself:
 
+    hidden rows -> layer norm -> 4-bit rows -> 4-bit product with the student's head
+           -> a token each (verification of nothing drafted), token by token
     hidden rows of all drafted positions -> layer norm -> 4-bit rows -> 4-bit product with the teacher's head
            -> verification against the student's logits, from given random numbers
 
@@ -52,6 +54,8 @@ class Step:
         self.y = torch.empty(rows, head.hs, dtype=torch.bfloat16, device="cuda")
         self.x4 = Rows4(rows, head.hs)
         self.out = torch.empty(rows, head.V, dtype=torch.bfloat16, device="cuda")
+        self.none = torch.zeros(rows + 1, dtype=torch.int64, device="cuda")           # starts of sequences with nothing drafted
+        self.nil = torch.empty(rows, dtype=torch.int32, device="cuda")
 
     def logits(self, x):
         """Logits (bf16) of hidden rows x [n][hs] bf16."""
@@ -62,6 +66,13 @@ class Step:
         vl.vl_gemm_fp4_tn_bf16(self.x4.q, self.x4.sf, self.x4.rs, h.plane.q, h.plane.sf, h.plane.rs, out, n, h.V, h.hs, h.V,
                                vl.VL_FP4_NV)
         return out
+
+    def draw(self, x, heat, pick, tokens):
+        """A token for each hidden row, from its softmax at temperature heat[i] and the random number pick[i]."""
+        n, V = x.shape[0], self.head.V
+        t = self.logits(x)
+        vl.vl_verify_draft_bf16(t, V, None, V, V, self.none, n, 0, None, heat, None, pick, tokens, self.nil)
+        return t
 
     def verify(self, x, draft, start, drafted, heat, u, pick, tokens, accepted, logp=None):
         """One pass of the teacher: hidden rows x of the drafted positions and of the one after them, sequence by
@@ -89,14 +100,14 @@ def decode(seqs, k, hs, V, passes, noise, heat, seed=1):
     drafted = torch.empty(seqs, k, dtype=torch.int32, device="cuda")
     tokens = torch.empty(seqs, k + 1, dtype=torch.int32, device="cuda")
     accepted = torch.empty(seqs, dtype=torch.int32, device="cuda")
+    said = torch.empty(seqs, dtype=torch.int32, device="cuda")
     last, kept, given = torch.randint(0, V, (seqs,), device="cuda", generator=g), 0, 0
     for _ in range(passes):
         seen = torch.empty(seqs, k + 1, dtype=torch.int64, device="cuda")
         seen[:, 0] = last
         for j in range(k):                                          # the student goes ahead, token by token
-            draft[:, j] = student.logits(table[seen[:, j]])
-            p = torch.softmax(draft[:, j].float() / heat, 1)
-            seen[:, j + 1] = torch.multinomial(p, 1, generator=g)[:, 0]
+            draft[:, j] = student.draw(table[seen[:, j]], temp, torch.rand(seqs, device="cuda", generator=g), said)
+            seen[:, j + 1] = said
         drafted.copy_(seen[:, 1:])
         u, pick = (torch.rand(n, device="cuda", generator=g) for n in (seqs * k, seqs))
         teacher.verify(table[seen.view(-1)], draft.view(seqs * k, V), start, drafted.view(-1), temp, u, pick, tokens.view(-1), accepted)
