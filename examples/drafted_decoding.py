@@ -33,6 +33,8 @@ class Rows4:
 
     def take(self, x):
         """Quantises bf16 rows x [n <= rows][cols]."""
+        if x.dim() != 2 or x.shape[0] > self.rows or x.shape[1] != self.cols or not x.is_contiguous():
+            raise ValueError(f"rows {tuple(x.shape)} do not fit buffers of [{self.rows}][{self.cols}]")
         vl.vl_quant_fp4_rows_bf16(x, self.cols, x.shape[0], self.cols, vl.VL_FP4_NV, self.q, self.sf, self.rs)
         return self
 
@@ -60,6 +62,8 @@ class Step:
     def logits(self, x):
         """Logits (bf16) of hidden rows x [n][hs] bf16."""
         h, n = self.head, x.shape[0]
+        if x.dim() != 2 or n > self.y.shape[0] or x.shape[1] != h.hs or not x.is_contiguous():
+            raise ValueError(f"hidden rows {tuple(x.shape)} do not fit a step of [{self.y.shape[0]}][{h.hs}]")
         y, out = self.y[:n], self.out[:n]
         vl.vl_layernorm_fwd_bf16(x, h.hs, n, h.hs, h.gamma, h.beta, 1e-5, y, h.hs)
         self.x4.take(y)
@@ -70,6 +74,8 @@ class Step:
     def draw(self, x, heat, pick, tokens):
         """A token for each hidden row, from its softmax at temperature heat[i] and the random number pick[i]."""
         n, V = x.shape[0], self.head.V
+        if not n == heat.numel() == pick.numel() == tokens.numel():
+            raise ValueError(f"{n} hidden rows, {heat.numel()} temperatures, {pick.numel()} random numbers, {tokens.numel()} tokens")
         t = self.logits(x)
         vl.vl_verify_draft_bf16(t, V, None, V, V, self.none, n, 0, None, heat, None, pick, tokens, self.nil)
         return t
@@ -77,6 +83,8 @@ class Step:
     def verify(self, x, draft, start, drafted, heat, u, pick, tokens, accepted, logp=None):
         """One pass of the teacher: hidden rows x of the drafted positions and of the one after them, sequence by
         sequence; the drafter's logits (None: proposals without probabilities), its tokens and the random numbers."""
+        if x.shape[0] != drafted.numel() + pick.numel():
+            raise ValueError(f"{x.shape[0]} hidden rows for {drafted.numel()} drafted tokens of {pick.numel()} sequences")
         t, V = self.logits(x), self.head.V
         vl.vl_verify_draft_bf16(t, V, draft, V, V, start, pick.numel(), drafted.numel(), drafted, heat, u, pick, tokens, accepted, logp)
         return t
