@@ -133,6 +133,16 @@ def test_rows_that_end_anywhere(short, bf16):
         check(M, N - short, 2600, O.NV, bf16, pad=short)
 
 
+@pytest.mark.parametrize("N", [1, 4, 8, 16, 24, 31, 40])
+@pytest.mark.parametrize("fmt", [O.NV, O.MX])
+def test_few_columns(N, fmt):
+    """Rows of D shorter than a copy's piece, alone and in wider rows."""
+    for M, K in ((70, 2600), (130, 2600), (200, 4096), (300, 2900)):
+        for bf16 in (False, True):
+            check(M, N, K, fmt, bf16)
+            check(M, N, K, fmt, bf16, pad=-N % 8 + 8)
+
+
 @pytest.mark.parametrize("off,pad", [(1, 0), (2, 2), (4, 4), (8, 1)])
 @pytest.mark.parametrize("fmt", [O.NV, O.MX])
 def test_pairs_at_any_place(off, pad, fmt):
