@@ -75,6 +75,16 @@ def test_scales_from_end_to_end(M, N, K, pad, bf16, way):
     product(M, N, K, ea, eb, 1.0, bf16, pad, blocks)
 
 
+@pytest.mark.parametrize("M,N,K", [(20000, 300, 300), (30001, 40, 64), (6000, 1100, 500)])
+@pytest.mark.parametrize("rows", [[-1], [0], [5000], [1, 127, 128, 4095, 5999]])
+def test_a_few_scales_among_many_rows(M, N, K, rows):
+    """Many tiles of rows, each met by some CTAs only: a row whose scale needs care anywhere among them."""
+    g = np.random.default_rng(K)
+    ea, eb = g.integers(-8, 8, M), g.integers(-112, -60, N)
+    ea[rows] = 115
+    product(M, N, K, ea, eb, 1.0, False, 0, (0x68, 0x70, 0x78))
+
+
 @pytest.mark.parametrize("M,N,K,pad", [(5, 300, 512, 0), (20, 200, 4100, 0), (200, 500, 4096, 0), (300, 9000, 2600, 0)])
 @pytest.mark.parametrize("alpha,ea,eb", [(2.0 ** 90, -110, 50), (-2.0 ** -100, 110, -60), (2.0 ** 127, -110, 5), (2.0 ** -149, 100, 40),
                                          (2.0 ** 70, 0, 0), (-0.375, 20, -20)])

@@ -644,10 +644,20 @@ __global__ void __launch_bounds__(384, 1)
         constexpr int CH = NT / 32, SH = C::SHARED / 32;       // a warp's chunks of 16 columns, and those shared
         float* const rx = S.rx[warp - 4];
         uint32_t tile = 0;
-        // asked once, of all rows: tile by tile even the question cost 1 to 5%
+        // asked once, of all rows that this CTA meets: in the loop below even the question cost 1 to 5%
         if (FMT == kNv && P.splits == 1) {
+            const int i = threadIdx.x - 128;
             bool any = false;
-            for (int m = threadIdx.x - 128; m < P.M; m += 256) any = any || beyond(P.rx[m]);
+            // tile by tile, until the same rows come again
+            const int count = min(mt, (tiles - cid + ncl - 1) / ncl), step = ncl % mt;
+            int mi = cid % mt;
+#pragma unroll 8
+            for (int j = 0; j < count; ++j) {
+                const int m = mi * NT + i;
+                any = any | beyond(i < NT && m < P.M ? P.rx[m] : 1.f);
+                mi += step;
+                mi -= mi >= mt ? mt : 0;
+            }
             if (any) S.far = 1;
             named_sync(1, 256);
         }
