@@ -507,7 +507,7 @@ VL_API vl_status vl_gemm_fp8_tn(const uint8_t* A, const float* sa, const uint8_t
  * when written; the factors in an order that keeps what is between them in fp32 where the result is, for alpha 0 or of magnitude
  * 2^-100 upwards).  Products are exact, sums fp32 in the tensor cores; A [M][Kp/2], B [N][Kp/2] with scales as above,
  * D [M][ldd].  K is any length from 1.  Logits from hidden rows and a head plane W [V][hs]; and dx = g . Wt^T over the transposed
- * plane Wt [hs][V], quantised by itself (its blocks run along V). 
+ * plane Wt [hs][V], quantised by itself (its blocks run along V).
  */
 #define VL_FP4_NV 0
 #define VL_FP4_MX 1
@@ -547,8 +547,11 @@ VL_API vl_status vl_gemm_fp4_tn_bf16(const uint8_t* A, const uint8_t* sfa, const
  *   accepted [nseq] int32: how many were accepted
  *   logp [ndraft + nseq] fp32 (nullable): ln p of each of these tokens (greedy: at temperature 1), 0 past the last
  * Data errors, counted into *err (nullable) once a sequence: a drafted token >= V is refused; a row of target or draft
- * that is reached and has no softmax (a NaN, +inf, or no column that is not banned), or a temperature out of range, ends the sequence there with 0xFFFFFFFF
- * as its next token.  Rows after the first refused token are not read.  A sequence's result does not depend on the others.
+ * that is reached and has no softmax (a NaN, +inf, or no column that is not banned), or a temperature out of range, ends the
+ * sequence there with 0xFFFFFFFF as its next token.  Rows after the first refused token, with their tokens and random numbers,
+ * never matter, but may be read (two to eight positions at once): they have to be readable memory that nothing writes meanwhile.
+ * A sequence's result does not depend on the others, bit for bit where its rows begin at 16 bytes, or at the same place within
+ * 16; at another place (rows of another number of bytes) the sums are taken in another order.
  * V is at most 2^30; the magnitude of a row's largest logit 2^30 times the temperature (beyond it a row may have no softmax).
  * Outputs may not overlap inputs.
  */

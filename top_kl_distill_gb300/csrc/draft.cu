@@ -10,9 +10,10 @@
 // A cluster of CTAs takes a sequence: its warps share out the rows' segments (1024 columns or more) in pieces of 2 KB, each piece in
 // registers between the maximum and the sum, with the next one's loads under way, and send each segment's (max, sum) to
 // every CTA of the cluster; after one cluster barrier all CTAs hold the same partials and come to the same
-// decision.  Rows after the first refused one are not read: a sweep takes `per` positions at once (one where there
-// are sequences enough to fill the GPU, all where latency counts).  The partials are by column, not by CTA, so a row's
-// statistics and its draw do not depend on the cluster's size or on the other sequences.
+// decision.  A sweep takes `per` positions at once, two to four, or eight where rows are short (see `verify_go`), so up to
+// seven rows after the first refused one are read too; they never matter.  The partials are by column, not by CTA, so a row's
+// statistics and its draw do not depend on the cluster's size or on the other sequences, but for the place within 16 bytes at
+// which the row begins: chunks, and with them the order of the sums, are aligned where the row is.
 //
 // Statistics are in units of log2: m2 is the largest x sc, sc = log2(e) / temperature, rounded to fp32, and only a
 // reference: with x sc - m2 in one fma (its error is half an ulp of the difference, nothing near the top) the sums are
@@ -23,7 +24,7 @@
 // 256 sequences of 8 drafted tokens over 128256 bf16 columns: 130 us, 546 MB read (4.2 TB/s; 490 MB are the rows that count);
 // 32 of 5: 27 us; one of 4 over 32000 fp32: 9.7.  A sweep's end (cluster barrier, decision) is 2 to 3 us in which its CTAs
 // read nothing, the draw 5; the four CTAs of an SM hide that from one another where there are enough, and the longest sequences
-// run on alone (85% of the SMs' time is in use).  Tried: the next sweep's rows brought into L2 ahead (27 to 30 us, 130 to 143), its
+// run on alone.  Tried: the next sweep's rows brought into L2 ahead (27 to 30 us, 130 to 143), its
 // first pieces loaded before the barrier (27.3 to 28.4, 129 to 133: the barrier waits for them), clusters of 16 CTAs (one
 // sequence 9.3 to 8.2 us, but 32 of them 31 to 39).
 #include "vl_api.h"
