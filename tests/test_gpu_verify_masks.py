@@ -78,3 +78,36 @@ def test_nothing_left(temp, dtype):
     tokens, acc, lp, err = call(t, None, np.array([0, 0, 0], np.int64), np.zeros(0, np.uint32), np.full(2, temp, np.float32),
                                 np.zeros(0, np.float32), np.full(2, 0.5, np.float32), dtype)
     assert tokens.view(np.uint32).tolist() == [0xFFFFFFFF, 7] and err == 1 and lp.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("mask", ["lowest", -1e10, -1e30])
+@pytest.mark.parametrize("temp", [1.0, 1.5, 0.3, 30.0, 0.0])
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_drafted_tokens_that_are_masked(mask, temp, draft, dtype):
+    """A token that the target bans is refused, whatever the drafter says of it and whatever u is; one that the drafter alone bans is
+    accepted (p / 0): as with -inf."""
+    mask = LOWEST[dtype] if mask == "lowest" else mask
+    n, k, V = 24, 3, 3000
+    t, y, s, tok, h, u, p = make([k] * n, V, 41, temp=[temp], draft=draft, dtype=dtype)
+    rows = np.arange(n * k) + np.repeat(np.arange(n), k)
+    for i in range(n * k):
+        if i % 4 in (0, 1):                                      # the target's ban, and with it the drafter's or not
+            t[rows[i], tok[i]] = -np.inf
+        if draft and i % 4 in (1, 2):
+            y[i, tok[i]] = -np.inf
+    t[:, 2000:2300] = -np.inf
+    if draft:
+        y[:, 1990:2310] = -np.inf
+    u[::5] = 0.0
+    if temp != 0.0:
+        t, y, s, tok, h, u, p = settle(t, y, s, tok, h, u, p, np.random.default_rng(1))
+    want = call(t, y, s, tok, h, u, p, dtype)
+    t = np.where(np.isinf(t), np.float32(mask), t)
+    y = np.where(np.isinf(y), np.float32(mask), y) if draft else None
+    got = call(t, y, s, tok, h, u, p, dtype)
+    for i in range(n):                                           # none of the banned tokens comes out
+        for j in range(int(got[1][i])):
+            assert t[rows[k * i + j], tok[k * i + j]] > mask
+    for a, b in zip(got, want):
+        assert np.array_equal(a, b)

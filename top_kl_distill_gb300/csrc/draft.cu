@@ -49,6 +49,7 @@ constexpr int ROWS = 2 * MAX_PER + 1;
 constexpr uint32_t kNone = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLow = -2147483648.f;    // half an ulp of what is above is 64 at most
+constexpr float kNever = -745.f;         // ln of a probability that is 0 in 64 bits too
 
 struct Smem {
     float2 part[2][ROWS][MAX_SEGS];      // (m2, sum of 2^(x sc - m2)) of a segment; by sweep, in turn
@@ -341,7 +342,8 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) verify(const VerifyPar
                     } else if (with_q) {
                         const float qm = S.rm[np + lane], qz = S.rz[np + lane];
                         fine = fine && qz > 0.f && qz < INFINITY;
-                        verdict = S.u[buf][lane] < ex2(x2 - fmaf(S.yd[buf][lane], sc, -qm)) * (qz / z) ? 0 : 1;
+                        // (a ratio of two masks is anything: where p is 0 it does not count)
+                        verdict = lp > kNever && S.u[buf][lane] < ex2(x2 - fmaf(S.yd[buf][lane], sc, -qm)) * (qz / z) ? 0 : 1;
                     } else {
                         verdict = S.u[buf][lane] < ex2(x2) / z ? 0 : 1;
                     }
