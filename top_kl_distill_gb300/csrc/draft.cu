@@ -339,13 +339,18 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) verify(const VerifyPar
                     lp = (x2 - __log2f(z)) * kLn2;
                     if (greedy) {
                         verdict = d == (uint32_t)S.rat[lane] ? 0 : 1;
-                    } else if (with_q) {
-                        const float qm = S.rm[np + lane], qz = S.rz[np + lane];
-                        fine = fine && qz > 0.f && qz < INFINITY;
-                        // (a ratio of two masks is anything: where p is 0 it does not count)
-                        verdict = lp > kNever && S.u[buf][lane] < ex2(x2 - fmaf(S.yd[buf][lane], sc, -qm)) * (qz / z) ? 0 : 1;
                     } else {
-                        verdict = S.u[buf][lane] < ex2(x2) / z ? 0 : 1;
+                        float ratio;
+                        if (with_q) {
+                            const float qm = S.rm[np + lane], qz = S.rz[np + lane];
+                            fine = fine && qz > 0.f && qz < INFINITY;
+                            ratio = ex2(x2 - fmaf(S.yd[buf][lane], sc, -qm)) * (qz / z);
+                        } else {
+                            ratio = ex2(x2) / z;
+                        }
+                        // where p is 0 the ratio does not count (it may be one of two masks); u = 0 is below any other p
+                        const float u = S.u[buf][lane];
+                        verdict = lp > kNever && (u < ratio || u == 0.f) ? 0 : 1;
                     }
                     if (d >= (uint32_t)V) verdict = 1;
                 }
