@@ -5,7 +5,7 @@ below 2^20, so that fp32 holds each of them in any order and D is the exact resu
 lost, counted twice or given another's scale then changes D, however long K is: the comparison is of bits.
 
 Which kernel a shape runs is decided by its sizes and the number of SMs; the tests name the kernel that they are for, and check
-by its name that it ran.
+by its name that it ran (on a GPU of 152 SMs, which the names are for).
 """
 import numpy as np
 import pytest
@@ -81,7 +81,7 @@ def check(M, N, K, fmt, bf16=False, pad=0, off=0, alpha=0.5, kernel=None):
     off_by = got[:, :N] != want.float().to(dt)
     assert not off_by.any(), (M, N, K, fmt, int(off_by.sum()), off_by.nonzero()[:4].tolist())
     assert (got[:, N:] == 5).all() and (buf[:off] == 5).all() and (buf[off + M * ld:] == 5).all()
-    if kernel is not None:
+    if kernel is not None and torch.cuda.get_device_properties(0).multi_processor_count == 152:
         ran = names(call)
         if not ran:
             pytest.skip("no kernel names to be had here (the results are right)")
